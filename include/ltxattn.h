@@ -340,6 +340,192 @@ LTXATTN_API int ltxattn_combine(const float* o_parts, const float* lses, void* o
                                 int q_len, int batch, int heads, int head_dim,
                                 ltxattn_stream_t stream);
 
+/* Element types of the calls that take more than bf16. */
+typedef enum ltxattn_dtype {
+  LTXATTN_BF16 = 0,
+  LTXATTN_FP16 = 1,
+  LTXATTN_FP32 = 2
+} ltxattn_dtype;
+
+/* Channel pairs that ltxattn_rope_axes turns together. */
+typedef enum ltxattn_rope_layout {
+  LTXATTN_ROPE_PAIRS = 0, /* (2i, 2i + 1), as ltxattn_qk_norm_rope */
+  LTXATTN_ROPE_HALVES = 1 /* (i, i + head_dim / 2) */
+} ltxattn_rope_layout;
+
+/* Arguments of ltxattn_rope_axes. */
+typedef struct ltxattn_rope_call {
+  const void* q;
+  const void* k; /* NULL: queries only (k_out NULL too) */
+  void* q_out;
+  void* k_out;
+  long long q_stride[3]; /* elements between batch rows, tokens, heads */
+  long long k_stride[3];
+  long long q_out_stride[3];
+  long long k_out_stride[3];
+  const float* positions; /* device, [positions_batch][len][axes] */
+  const double* inv_freq; /* host, sum(axis_dims) / 2 radians per unit of position */
+  int axis_dims[4];       /* channels of every head that turn with axis a, even */
+  int axes;               /* 1 .. 4 */
+  int positions_batch;    /* batch, or 1: the same positions in every batch row */
+  int batch, len, heads, kv_heads, head_dim;
+  int dtype;   /* ltxattn_dtype of q, k and the outputs */
+  int layout;  /* ltxattn_rope_layout */
+  int inverse; /* nonzero: turn by the negative angles (the gradient of the rotation) */
+} ltxattn_rope_call;
+
+/*
+ * Rotary positions with several axes (time, height and width of a video token).  Queries and
+ * keys [batch, len, heads | kv_heads, head_dim]; the channel pairs of a head are dealt out to
+ * the axes in order, pair i of axis a turning by
+ *     angle = positions[b, l, a] * inv_freq[i]
+ *     (x_i, x_j) -> (x_i cos - x_j sin, x_i sin + x_j cos)
+ * and the pairs behind the last axis (sum(axis_dims) < head_dim) stay as they are.  Positions
+ * may be fractional, negative and different in every batch row (clips of their own grids in
+ * one batch); angles are formed with 48 bits of inv_freq and reduced before the sine, so far
+ * positions (to 2^24) lose nothing.  The gradient of a rotation is the rotation back: call it
+ * on the gradients with inverse set.
+ *
+ *   q, k, outputs  device; any strides that are multiples of 16 bytes, the head_dim channels
+ *                  contiguous (views of a fused projection; head-major tensors).  Each output
+ *                  may be its own input (same address and strides) and must otherwise share
+ *                  no byte with q, k, the other output or positions: their address ranges are
+ *                  apart, or they are parts of the same rows (INVALID_ARG when neither shows)
+ *   head_dim       a multiple of 8 (16 in the halves layout), at most 512; axes <= 4
+ *   batch * len    below 2^31
+ * Arithmetic in fp32, one rounding at the end.  Needs no ltxattn_create.  Base addresses and
+ * strides 16-byte aligned, positions 4-byte (MISALIGNED).  Checks run on the host before any
+ * CUDA call (INVALID_ARG, UNSUPPORTED, MISALIGNED); LTXATTN_ERR_CUDA on a failed launch.
+ * Asynchronous on `stream`; inv_freq and the struct are read during the call only.
+ */
+LTXATTN_API int ltxattn_rope_axes(const ltxattn_rope_call* call, ltxattn_stream_t stream);
+
+/* Largest sizes of the layer norm calls (larger values give LTXATTN_ERR_UNSUPPORTED). */
+#define LTXATTN_MAX_NORM_ROWS (1LL << 30)
+#define LTXATTN_MAX_NORM_COLS (1 << 20)
+
+/*
+ * Layer norm of every row of x [rows, cols]:
+ *     mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *     out = (x - mean) * rstd * weight[g] + bias[g],   g = row / (rows / groups)
+ * The rows come in `groups` equal runs with a weight and bias each: 1 for a model's own
+ * parameters, the batch size for the scale and shift per sample of a diffusion transformer.
+ *
+ *   x, out        device, element type dtype, x_stride / out_stride elements between rows
+ *                 (>= cols); out may be x (same address and stride), else no overlap
+ *   weight, bias  device, [groups][cols] of dtype; weight NULL: 1; bias NULL: 0 (a bias needs
+ *                 a weight)
+ *   mean, rstd    device fp32 [rows], written, or NULL; what the backward call reads
+ *   rows % groups == 0; eps finite, >= 0
+ * Sums and statistics in fp32, the variance around the mean; one rounding at the end.  Rows
+ * and weights on 16-byte boundaries with cols a multiple of 16 bytes run on 16-byte loads;
+ * any other alignment of whole elements works, slower.  Needs no ltxattn_create.  Checks run
+ * on the host before any CUDA call (INVALID_ARG, UNSUPPORTED, MISALIGNED); LTXATTN_ERR_CUDA
+ * on a failed launch.  Asynchronous on `stream`.
+ */
+LTXATTN_API int ltxattn_layer_norm(const void* x, const void* weight, const void* bias, void* out,
+                                   float* mean, float* rstd, long long rows, int cols,
+                                   long long groups, long long x_stride, long long out_stride,
+                                   float eps, int dtype, ltxattn_stream_t stream);
+
+/*
+ * Bytes of device workspace that ltxattn_layer_norm_backward needs on the current device for
+ * these sizes when dweight or dbias is wanted (0 otherwise).
+ */
+LTXATTN_API int ltxattn_layer_norm_workspace(long long rows, int cols, long long groups,
+                                             int dtype, unsigned long long* bytes);
+
+/*
+ * Gradients of ltxattn_layer_norm:
+ *     z = (x - mean) * rstd,  g = dy * weight
+ *     dx = rstd * (g - sum g / cols - z * sum (g z) / cols)
+ *     dweight[group] = sum over its rows of dy * z,  dbias[group] = sum of dy
+ *   dy, x, weight, mean, rstd   as the forward call took and wrote them (weight NULL: 1)
+ *   dx        dtype, [rows, cols]; may be dy or x (same address and stride)
+ *   dweight, dbias  device fp32 [groups][cols], written, either may be NULL
+ *   workspace device, 4-byte aligned, at least what ltxattn_layer_norm_workspace says; not
+ *             needed without dweight and dbias.  Calls that may overlap in time need one each.
+ * fp32 sums, added in a fixed order (the same call gives the same bits).  Same checks as
+ * ltxattn_layer_norm; a workspace that is missing or too small is INVALID_ARG.
+ */
+LTXATTN_API int ltxattn_layer_norm_backward(
+    const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+    void* dx, float* dweight, float* dbias, long long rows, int cols, long long groups,
+    long long dy_stride, long long x_stride, long long dx_stride, int dtype, void* workspace,
+    unsigned long long workspace_bytes, ltxattn_stream_t stream);
+
+/* Most documents per batch row of the masked calls. */
+#define LTXATTN_MAX_DOCS 65535
+
+/* Arguments of ltxattn_masked_forward and ltxattn_masked_backward. */
+typedef struct ltxattn_masked_call {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;            /* device fp32 [batch][heads][q_len]; NULL: not wanted (forward) */
+  long long q_stride[3]; /* elements between batch rows, tokens, heads */
+  long long k_stride[3];
+  long long v_stride[3];
+  long long out_stride[3];
+  int batch, q_len, kv_len, heads, kv_heads, head_dim;
+  float scale;
+  float softcap;         /* 0: none */
+  const float* slopes;   /* device [heads], or NULL: no bias */
+  const int* prefix;     /* device [batch][max(docs, 1)], or NULL: 0 (causal only) */
+  const int* q_starts;   /* device [batch][docs + 1], or NULL (docs == 0) */
+  const int* kv_starts;
+  int docs;              /* documents per batch row; 0: one, the whole row */
+  int causal;
+} ltxattn_masked_call;
+
+/*
+ * Attention with masked, capped and distance-biased scores: several clips packed into one
+ * sequence, a text prefix ahead of tokens in order, capped logits.  Batch row b holds `docs`
+ * documents: document d has the queries [q_starts[b][d], q_starts[b][d + 1]) and the keys
+ * [kv_starts[b][d], kv_starts[b][d + 1]) (without offsets: all of them), and nothing else is
+ * visible to its queries.  For its query i of nq and key j of nk, with p = i + nk - nq (the
+ * last query stands at the last key):
+ *     s = scale * q_i . k_j
+ *     s = softcap * tanh(s / softcap)             if softcap > 0
+ *     s = s - slopes[h] * |p - j|                 if slopes
+ *     visible: not causal, or j <= p, or j < prefix[b][d]
+ *     out_i = sum_j softmax(s)_j v_j,  lse_i = log2 sum_j exp(s_j)
+ * Query head h uses key head h / (heads / kv_heads).  A query that sees no key gets out = 0 and
+ * lse = -inf.  Rows of no document (ahead of the first offset, behind the last) are not read
+ * as queries and their out and lse are left as they were.  Key and value rows outside a
+ * document never reach its results, whatever they hold (infinities and NaN included); a value
+ * row of the document itself that is not finite may reach every query of the document.
+ *
+ *   q, out  bf16 [batch, q_len, heads, head_dim]; k, v bf16 [batch, kv_len, kv_heads,
+ *           head_dim]; device, channels contiguous, other strides any positive multiple of
+ *           16 bytes.  out must share no byte with q, k, v or a smaller array (address ranges
+ *           apart, or parts of the same rows), nor lse with anything.
+ *   head_dim 64 or 128; heads % kv_heads == 0; sizes as ltxattn_forward; docs <= 65535
+ *   q_starts, kv_starts  not decreasing along a batch row, from 0 to q_len / kv_len.  They are
+ *           read on the device; offsets that break this give unspecified values in out and
+ *           lse, never an access outside the tensors.
+ *   scale finite, > 0; softcap finite, >= 0; slopes finite
+ *   workspace  device, 16-byte aligned, at least what ltxattn_masked_workspace says.  Calls
+ *           that may overlap in time (two streams, two captured graphs) need one each.
+ * bf16 products, fp32 scores and statistics, P rounded to bf16 before the PV product, output
+ * rounded once.  Needs ltxattn_create on the current device.  Host checks as ltxattn_forward,
+ * before any CUDA call (INVALID_ARG, UNSUPPORTED, MISALIGNED); a workspace that is missing or
+ * too small is INVALID_ARG; LTXATTN_ERR_CUDA on a failed launch; a kernel wait that times out
+ * is reported by ltxattn_check.  Asynchronous on `stream`.
+ */
+LTXATTN_API int ltxattn_masked_forward(const ltxattn_masked_call* call, void* workspace,
+                                       unsigned long long workspace_bytes,
+                                       ltxattn_stream_t stream);
+
+/*
+ * Bytes of device workspace the masked call needs on the current device (backward != 0: the
+ * backward call).  Sizes, docs and causal are read; pointers only for being NULL or not.
+ * Needs ltxattn_create.
+ */
+LTXATTN_API int ltxattn_masked_workspace(const ltxattn_masked_call* call, int backward,
+                                         unsigned long long* bytes);
+
 /* Size of the library's built-in scratch array used by ltxattn_forward_split_noalloc. */
 #define LTXATTN_NOALLOC_SCRATCH_BYTES (16u << 20) /* 16 MiB per GPU */
 

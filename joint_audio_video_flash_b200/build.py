@@ -9,11 +9,14 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libltxattn.so")
 DEBUG_LIB = os.path.join(PKG, "libltxattn_debug.so")  # -DLTXATTN_DEBUG: workspace guard words
-SOURCES = ["ltxattn.cu"]
+SOURCES = ["ltxattn.cu", "masked.cu", "block_ops.cu"]
 DEPS = ["ltxattn.cu", "attn_fwd.cuh", "attn_fwd_pp.cuh", "attn_fwd_skv.cuh", "attn_fwd_pair.cuh",
         "attn_fwd_a2v.cuh", "qk_prologue.cuh",
-        "na3d_fwd.cuh", "combine.cuh", "debug_guard.cuh", "sm100_ptx.cuh"]
-NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
+        "na3d_fwd.cuh", "combine.cuh", "debug_guard.cuh", "sm100_ptx.cuh", "masked.cu",
+        "attn_masked_fwd.cuh", "block_ops.cu", "rope_axes.cuh", "layer_norm.cuh", "dtype.cuh",
+        "device_context.h", "host_common.h"]
+NVCC_FLAGS = ["--threads", "0",  # the sources compile side by side
+              "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-shared"]
 
 
@@ -33,7 +36,7 @@ def _stale(lib: str) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    """Compile csrc/ltxattn.cu (+ headers) into joint_audio_video_flash_b200/libltxattn.so, or,
+    """Compile csrc/*.cu (+ headers) into joint_audio_video_flash_b200/libltxattn.so, or,
     with debug=True, the guard-word build libltxattn_debug.so (-DLTXATTN_DEBUG)."""
     lib = DEBUG_LIB if debug else LIB
     if not force and not _stale(lib):

@@ -1,0 +1,507 @@
+// block_ops.cu -- host side of the operators around attention that need no context: rotary
+// positions with several axes and layer norm with its gradients.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "host_common.h"
+#include "layer_norm.cuh"
+#include "rope_axes.cuh"
+
+namespace {
+
+using ltx::ranges_overlap;
+
+int elem_size(int dtype) {
+  switch (dtype) {
+    case LTXATTN_BF16:
+    case LTXATTN_FP16: return 2;
+    case LTXATTN_FP32: return 4;
+    default: return 0;
+  }
+}
+
+// ---------------------------------------------------------------- rotary axes
+// A [batch, len, heads, head_dim] view with strides in elements.
+struct View {
+  const char* base;
+  long long batch, len, heads, dim;  // extents
+  long long sb, sl, sh;              // strides
+  int item;
+};
+
+// Bytes from the first to behind the last element.
+size_t view_bytes(const View& v) {
+  return (size_t)((v.batch - 1) * v.sb + (v.len - 1) * v.sl + (v.heads - 1) * v.sh + v.dim) *
+         v.item;
+}
+
+// True when the views share no byte: their ranges are apart, or they are slices of the same
+// rows (same batch and token strides) whose parts of a row are apart, as the queries and keys
+// of one fused projection are.
+bool views_apart(const View& a, const View& b) {
+  if (!ranges_overlap(a.base, view_bytes(a), b.base, view_bytes(b))) return true;
+  const bool rows = a.len == 1 && b.len == 1 && a.batch > 1;  // the batch row is the row
+  const long long row = rows ? a.sb : a.sl;
+  if (row <= 0 || (rows ? b.sb : b.sl) != row) return false;
+  if (!rows && (a.batch > 1 || b.batch > 1) && (a.sb != b.sb || a.sb % row != 0)) return false;
+  const long long bytes = row * a.item;
+  const long long wa = ((a.heads - 1) * a.sh + a.dim) * a.item;
+  const long long wb = ((b.heads - 1) * b.sh + b.dim) * b.item;
+  long long off = (b.base - a.base) % bytes;
+  if (off < 0) off += bytes;
+  return off >= wa && off + wb <= bytes;
+}
+
+template <typename T>
+cudaError_t launch_rope(const ltx::RopeParams& p, bool halves, cudaStream_t stream) {
+  const long long rows = (long long)p.batch * p.len;
+  const unsigned grid = (unsigned)((rows + p.tokens - 1) / p.tokens);
+  if (halves)
+    ltx::ltx_rope_axes<T, true><<<grid, ltx::kRopeThreads, 0, stream>>>(p);
+  else
+    ltx::ltx_rope_axes<T, false><<<grid, ltx::kRopeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- layer norm
+// CTAs per group that fill the device once, and no more than there are row slots to take.
+int norm_ctas(int resident, long long groups, long long rows_per_group, int slots) {
+  const long long want = (rows_per_group + slots - 1) / slots;
+  return (int)std::max<long long>(1, std::min<long long>(want, resident / groups));
+}
+
+// Warps per row for `per_lane` elements a lane at most; 0 when a row does not fit a CTA.
+int norm_warps(int cols, int per_lane) {
+  for (int wpr = 1; wpr <= ltx::kNormWarps; wpr *= 2)
+    if ((long long)wpr * 32 * per_lane >= cols) return wpr;
+  return 0;
+}
+
+// Every row and the weights start on 16 bytes and hold whole 16-byte chunks.
+bool norm_vector(const ltx::NormParams& p, int item, bool grad) {
+  uintptr_t at = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out) |
+                 reinterpret_cast<uintptr_t>(p.weight) | reinterpret_cast<uintptr_t>(p.bias);
+  long long strides = (p.x_stride | p.out_stride | p.cols) * item;
+  if (grad) {
+    at |= reinterpret_cast<uintptr_t>(p.dy);
+    strides |= p.dy_stride * item;
+  }
+  return ((at | (uintptr_t)strides) & 15u) == 0;
+}
+
+template <typename T, int V, int kChunks>
+int launch_norm(ltx::NormParams& p, long long groups, int wpr, cudaStream_t stream) {
+  const int resident = ltx::resident_ctas<ltx::ltx_layer_norm<T, V, kChunks>>(ltx::kNormThreads);
+  if (resident < 1) return LTXATTN_ERR_CUDA;
+  p.wpr = wpr;
+  p.ctas_per_group = norm_ctas(resident, groups, p.rows_per_group, ltx::kNormWarps / wpr);
+  ltx::ltx_layer_norm<T, V, kChunks>
+      <<<(unsigned)(groups * p.ctas_per_group), ltx::kNormThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+}
+
+template <typename T>
+int layer_norm_forward(ltx::NormParams& p, long long groups, cudaStream_t stream) {
+  constexpr int V = ltx::Elem<T>::kVec;
+  if (norm_vector(p, (int)sizeof(T), false)) {
+    if (int w = norm_warps(p.cols, 4 * V)) return launch_norm<T, V, 4>(p, groups, w, stream);
+    if (int w = norm_warps(p.cols, 8 * V)) return launch_norm<T, V, 8>(p, groups, w, stream);
+  } else {
+    if (int w = norm_warps(p.cols, 8)) return launch_norm<T, 1, 8>(p, groups, w, stream);
+    if (int w = norm_warps(p.cols, 16)) return launch_norm<T, 1, 16>(p, groups, w, stream);
+  }
+  const int resident = ltx::resident_ctas<ltx::ltx_layer_norm_wide<T>>(ltx::kNormThreads);
+  if (resident < 1) return LTXATTN_ERR_CUDA;
+  p.wpr = ltx::kNormWarps;
+  p.ctas_per_group = norm_ctas(resident, groups, p.rows_per_group, 1);
+  ltx::ltx_layer_norm_wide<T>
+      <<<(unsigned)(groups * p.ctas_per_group), ltx::kNormThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+}
+
+// The plan of a backward call, the same for the workspace query and the launch.
+enum class GradKernel { kVector, kScalar8, kScalar16, kWide };
+struct GradPlan {
+  GradKernel kernel;
+  int wpr, ctas_per_group;
+  size_t workspace;  // bytes of partials
+};
+
+template <typename T, int V, int kChunks>
+int grad_resident(bool affine) {
+  return affine ? ltx::resident_ctas<ltx::ltx_layer_norm_grad<T, V, kChunks, true>>(
+                      ltx::kNormThreads)
+                : ltx::resident_ctas<ltx::ltx_layer_norm_grad<T, V, kChunks, false>>(
+                      ltx::kNormThreads);
+}
+
+template <typename T>
+int grad_plan(int cols, bool vector, bool affine, long long groups, long long rows_per_group,
+              GradPlan* plan) {
+  constexpr int V = ltx::Elem<T>::kVec;
+  int resident = 0;
+  if (vector && (plan->wpr = norm_warps(cols, 4 * V))) {
+    plan->kernel = GradKernel::kVector;
+    resident = grad_resident<T, V, 4>(affine);
+  } else if (!vector && (plan->wpr = norm_warps(cols, 8))) {
+    plan->kernel = GradKernel::kScalar8;
+    resident = grad_resident<T, 1, 8>(affine);
+  } else if (!vector && (plan->wpr = norm_warps(cols, 16))) {
+    plan->kernel = GradKernel::kScalar16;
+    resident = grad_resident<T, 1, 16>(affine);
+  } else {
+    plan->kernel = GradKernel::kWide;
+    plan->wpr = ltx::kNormWarps;
+    resident = ltx::resident_ctas<ltx::ltx_layer_norm_grad_wide<T>>(ltx::kNormThreads);
+  }
+  if (resident < 1) return LTXATTN_ERR_CUDA;
+  plan->ctas_per_group =
+      norm_ctas(resident, groups, rows_per_group, ltx::kNormWarps / plan->wpr);
+  plan->workspace = affine && plan->ctas_per_group > 1
+                        ? (size_t)groups * plan->ctas_per_group * 2 * cols * sizeof(float)
+                        : 0;
+  return LTXATTN_OK;
+}
+
+int grad_plan_of(int dtype, int cols, bool vector, bool affine, long long groups,
+                 long long rows_per_group, GradPlan* plan) {
+  switch (dtype) {
+    case LTXATTN_BF16:
+      return grad_plan<__nv_bfloat16>(cols, vector, affine, groups, rows_per_group, plan);
+    case LTXATTN_FP16:
+      return grad_plan<__half>(cols, vector, affine, groups, rows_per_group, plan);
+    default:
+      return grad_plan<float>(cols, vector, affine, groups, rows_per_group, plan);
+  }
+}
+
+template <typename T, int V, int kChunks>
+cudaError_t launch_grad(const ltx::NormParams& p, long long groups, bool affine,
+                        cudaStream_t stream) {
+  const unsigned grid = (unsigned)(groups * p.ctas_per_group);
+  // several row slots (cols <= 4 warps' worth, 32 KB at most) meet in shared memory
+  const size_t smem = affine && p.wpr < ltx::kNormWarps ? 2 * p.cols * sizeof(float) : 0;
+  if (affine)
+    ltx::ltx_layer_norm_grad<T, V, kChunks, true><<<grid, ltx::kNormThreads, smem, stream>>>(p);
+  else
+    ltx::ltx_layer_norm_grad<T, V, kChunks, false><<<grid, ltx::kNormThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+int layer_norm_grad(const ltx::NormParams& p, long long groups, bool affine,
+                    const GradPlan& plan, cudaStream_t stream) {
+  constexpr int V = ltx::Elem<T>::kVec;
+  cudaError_t e = cudaSuccess;
+  switch (plan.kernel) {
+    case GradKernel::kVector: e = launch_grad<T, V, 4>(p, groups, affine, stream); break;
+    case GradKernel::kScalar8: e = launch_grad<T, 1, 8>(p, groups, affine, stream); break;
+    case GradKernel::kScalar16: e = launch_grad<T, 1, 16>(p, groups, affine, stream); break;
+    case GradKernel::kWide: {
+      const unsigned grid = (unsigned)(groups * p.ctas_per_group);
+      if (affine) {  // ahead of dx, which may replace x or dy
+        const unsigned blocks = (unsigned)std::min(64, (p.cols + ltx::kNormThreads - 1) /
+                                                           ltx::kNormThreads);
+        ltx::ltx_layer_norm_grad_cols<T><<<dim3(grid, blocks), ltx::kNormThreads, 0, stream>>>(p);
+        e = cudaGetLastError();
+      }
+      if (e == cudaSuccess) {
+        ltx::ltx_layer_norm_grad_wide<T><<<grid, ltx::kNormThreads, 0, stream>>>(p);
+        e = cudaGetLastError();
+      }
+    }
+  }
+  if (e == cudaSuccess && p.partial) {
+    const int col_blocks = (2 * p.cols + 31) / 32;
+    ltx::ltx_layer_norm_grad_sum<<<(unsigned)(groups * col_blocks), ltx::kNormThreads, 0,
+                                   stream>>>(p.partial, p.dweight, p.dbias, p.ctas_per_group,
+                                             p.cols, col_blocks);
+    e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+}
+
+int norm_sizes(long long rows, int cols, long long groups, int dtype) {
+  if (rows < 1 || cols < 1 || groups < 1 || rows % groups != 0 || !elem_size(dtype))
+    return LTXATTN_ERR_INVALID_ARG;
+  if (rows > LTXATTN_MAX_NORM_ROWS || cols > LTXATTN_MAX_NORM_COLS ||
+      groups * ((2LL * cols + 31) / 32) > 0x7fffffffLL)
+    return LTXATTN_ERR_UNSUPPORTED;
+  return LTXATTN_OK;
+}
+
+size_t norm_bytes(long long rows, long long stride, int cols, int item) {
+  return (size_t)((rows - 1) * stride + cols) * item;
+}
+
+// `out` may be `in` itself (same address and stride); otherwise they share no byte.
+bool norm_alias_ok(const void* out, long long so, const void* in, long long si, long long rows,
+                   int cols, int item) {
+  if (out == in && so == si) return true;
+  return !ranges_overlap(out, norm_bytes(rows, so, cols, item), in,
+                         norm_bytes(rows, si, cols, item));
+}
+
+}  // namespace
+
+extern "C" {
+
+int ltxattn_rope_axes(const ltxattn_rope_call* call, ltxattn_stream_t stream_) {
+  if (!call) return LTXATTN_ERR_INVALID_ARG;
+  const ltxattn_rope_call& a = *call;
+  const int item = elem_size(a.dtype);
+  const bool with_k = a.k != nullptr;
+  if (!a.q || !a.q_out || with_k != (a.k_out != nullptr) || !a.positions || !a.inv_freq || !item)
+    return LTXATTN_ERR_INVALID_ARG;
+  if (a.batch < 1 || a.len < 1 || a.heads < 1 || a.head_dim < 1 || (with_k && a.kv_heads < 1) ||
+      a.axes < 1 || (a.layout != LTXATTN_ROPE_PAIRS && a.layout != LTXATTN_ROPE_HALVES) ||
+      (a.positions_batch != 1 && a.positions_batch != a.batch))
+    return LTXATTN_ERR_INVALID_ARG;
+  if (a.axes > ltx::kRopeMaxAxes) return LTXATTN_ERR_UNSUPPORTED;
+  int rotated = 0;
+  for (int i = 0; i < a.axes; ++i) {
+    if (a.axis_dims[i] < 0 || a.axis_dims[i] % 2 != 0 || a.axis_dims[i] > a.head_dim)
+      return LTXATTN_ERR_INVALID_ARG;
+    rotated += a.axis_dims[i];
+  }
+  if (rotated < 2 || rotated > a.head_dim) return LTXATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < rotated / 2; ++i)
+    if (!std::isfinite(a.inv_freq[i])) return LTXATTN_ERR_INVALID_ARG;
+  const bool halves = a.layout == LTXATTN_ROPE_HALVES;
+  if (a.head_dim % (halves ? 16 : 8) != 0 || a.head_dim > 2 * ltx::kRopeMaxPairs ||
+      a.len > LTXATTN_MAX_LEN || a.batch > LTXATTN_MAX_BATCH || a.heads > LTXATTN_MAX_HEADS ||
+      (with_k && a.kv_heads > LTXATTN_MAX_HEADS) || (long long)a.batch * a.len > 0x7fffffffLL)
+    return LTXATTN_ERR_UNSUPPORTED;
+
+  const void* ptrs[4] = {a.q, a.q_out, a.k, a.k_out};
+  const long long* strides[4] = {a.q_stride, a.q_out_stride, a.k_stride, a.k_out_stride};
+  View v[4];
+  for (int i = 0; i < (with_k ? 4 : 2); ++i) {
+    const int heads = i < 2 ? a.heads : a.kv_heads;
+    v[i] = View{static_cast<const char*>(ptrs[i]), a.batch, a.len, heads, a.head_dim,
+                strides[i][0], strides[i][1], strides[i][2], item};
+    // a stride counts only where there is a second row to step to
+    if (a.batch == 1) v[i].sb = 0;
+    if (a.len == 1) v[i].sl = 0;
+    if (heads == 1) v[i].sh = 0;
+    if (v[i].sb < 0 || v[i].sl < 0 || v[i].sh < 0) return LTXATTN_ERR_INVALID_ARG;
+    // rows of an output that lie on one another would race
+    if (i % 2 == 1 && ((a.batch > 1 && v[i].sb == 0) || (a.len > 1 && v[i].sl == 0) ||
+                       (heads > 1 && v[i].sh == 0)))
+      return LTXATTN_ERR_INVALID_ARG;
+  }
+  uintptr_t mis = 0;
+  for (int i = 0; i < (with_k ? 4 : 2); ++i)
+    mis |= reinterpret_cast<uintptr_t>(ptrs[i]) |
+           (uintptr_t)((v[i].sb | v[i].sl | v[i].sh) * item);
+  if ((mis & 15u) || (reinterpret_cast<uintptr_t>(a.positions) & 3u))
+    return LTXATTN_ERR_MISALIGNED;
+  auto same = [](const View& x, const View& y) {
+    return x.base == y.base && x.sb == y.sb && x.sl == y.sl && x.sh == y.sh &&
+           x.heads == y.heads;
+  };
+  if (!same(v[1], v[0]) && !views_apart(v[1], v[0])) return LTXATTN_ERR_INVALID_ARG;
+  if (with_k) {
+    if (!same(v[3], v[2]) && !views_apart(v[3], v[2])) return LTXATTN_ERR_INVALID_ARG;
+    if (!views_apart(v[1], v[2]) || !views_apart(v[1], v[3]) || !views_apart(v[3], v[0]))
+      return LTXATTN_ERR_INVALID_ARG;
+  }
+  const size_t pos_bytes = (size_t)a.positions_batch * a.len * a.axes * 4;
+  for (int i = 1; i < (with_k ? 4 : 2); i += 2)
+    if (ranges_overlap(v[i].base, view_bytes(v[i]), a.positions, pos_bytes))
+      return LTXATTN_ERR_INVALID_ARG;
+
+  ltx::RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  for (int t = 0; t < (with_k ? 2 : 1); ++t) {
+    p.x[t] = ptrs[2 * t];
+    p.out[t] = const_cast<void*>(ptrs[2 * t + 1]);
+    const View &in = v[2 * t], &out = v[2 * t + 1];
+    const long long si[3] = {in.sb, in.sl, in.sh}, so[3] = {out.sb, out.sl, out.sh};
+    for (int i = 0; i < 3; ++i) {
+      p.x_stride[t][i] = si[i];
+      p.out_stride[t][i] = so[i];
+    }
+  }
+  p.heads_q = a.heads;
+  p.heads = a.heads + (with_k ? a.kv_heads : 0);
+  p.batch = a.batch;
+  p.len = a.len;
+  p.head_dim = a.head_dim;
+  p.positions = a.positions;
+  p.pos_batch = a.positions_batch == 1 ? 0 : (long long)a.len * a.axes;
+  p.axes = a.axes;
+  int pair = 0;
+  for (int i = 0; i < a.axes; ++i) {
+    pair += a.axis_dims[i] / 2;
+    p.axis_end[i] = pair;
+  }
+  p.pairs = pair;
+  p.sign = a.inverse ? -1.0f : 1.0f;
+  for (int i = 0; i < pair; ++i) {
+    const double turns = a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    p.freq[i].x = (float)turns;
+    p.freq[i].y = (float)(turns - (double)p.freq[i].x);
+  }
+  const int chunk = 16 / item;
+  p.units = a.head_dim / (halves ? 2 * chunk : chunk);
+  const int slots = ltx::kRopeThreads / p.units;  // units <= 128
+  p.head_slots = std::min(p.heads, slots);
+  p.tokens = slots / p.head_slots;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const cudaError_t e = a.dtype == LTXATTN_BF16   ? launch_rope<__nv_bfloat16>(p, halves, stream)
+                        : a.dtype == LTXATTN_FP16 ? launch_rope<__half>(p, halves, stream)
+                                                  : launch_rope<float>(p, halves, stream);
+  return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+}
+
+int ltxattn_layer_norm(const void* x, const void* weight, const void* bias, void* out,
+                       float* mean, float* rstd, long long rows, int cols, long long groups,
+                       long long x_stride, long long out_stride, float eps, int dtype,
+                       ltxattn_stream_t stream_) {
+  if (!x || !out || (bias && !weight)) return LTXATTN_ERR_INVALID_ARG;
+  int st = norm_sizes(rows, cols, groups, dtype);
+  if (st == LTXATTN_ERR_INVALID_ARG) return st;
+  if (x_stride < cols || out_stride < cols || !std::isfinite(eps) || eps < 0.0f)
+    return LTXATTN_ERR_INVALID_ARG;
+  if (st != LTXATTN_OK) return st;
+  const int item = elem_size(dtype);
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out) |
+                        reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(bias);
+  if ((mis & (uintptr_t)(item - 1)) ||
+      ((reinterpret_cast<uintptr_t>(mean) | reinterpret_cast<uintptr_t>(rstd)) & 3u))
+    return LTXATTN_ERR_MISALIGNED;
+  const size_t out_bytes = norm_bytes(rows, out_stride, cols, item);
+  const size_t x_bytes = norm_bytes(rows, x_stride, cols, item);
+  const size_t affine = (size_t)groups * cols * item, stats = (size_t)rows * 4;
+  if (!norm_alias_ok(out, out_stride, x, x_stride, rows, cols, item) ||
+      (weight && ranges_overlap(out, out_bytes, weight, affine)) ||
+      (bias && ranges_overlap(out, out_bytes, bias, affine)))
+    return LTXATTN_ERR_INVALID_ARG;
+  for (float* s : {mean, rstd})
+    if (s && (ranges_overlap(s, stats, x, x_bytes) || ranges_overlap(s, stats, out, out_bytes) ||
+              (weight && ranges_overlap(s, stats, weight, affine)) ||
+              (bias && ranges_overlap(s, stats, bias, affine))))
+      return LTXATTN_ERR_INVALID_ARG;
+  if (mean && rstd && ranges_overlap(mean, stats, rstd, stats)) return LTXATTN_ERR_INVALID_ARG;
+  ltx::NormParams p{};
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.out = out;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.x_stride = x_stride;
+  p.out_stride = out_stride;
+  p.cols = cols;
+  p.rows_per_group = rows / groups;
+  p.eps = eps;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  switch (dtype) {
+    case LTXATTN_BF16: return layer_norm_forward<__nv_bfloat16>(p, groups, stream);
+    case LTXATTN_FP16: return layer_norm_forward<__half>(p, groups, stream);
+    default: return layer_norm_forward<float>(p, groups, stream);
+  }
+}
+
+int ltxattn_layer_norm_workspace(long long rows, int cols, long long groups, int dtype,
+                                 unsigned long long* bytes) {
+  if (!bytes) return LTXATTN_ERR_INVALID_ARG;
+  int st = norm_sizes(rows, cols, groups, dtype);
+  if (st != LTXATTN_OK) return st;
+  // addresses decide between the two register kernels: the larger of their needs
+  unsigned long long most = 0;
+  for (bool vector : {false, true}) {
+    GradPlan plan;
+    st = grad_plan_of(dtype, cols, vector, true, groups, rows / groups, &plan);
+    if (st != LTXATTN_OK) return st;
+    most = std::max<unsigned long long>(most, plan.workspace);
+  }
+  *bytes = most;
+  return LTXATTN_OK;
+}
+
+int ltxattn_layer_norm_backward(const void* dy, const void* x, const void* weight,
+                                const float* mean, const float* rstd, void* dx, float* dweight,
+                                float* dbias, long long rows, int cols, long long groups,
+                                long long dy_stride, long long x_stride, long long dx_stride,
+                                int dtype, void* workspace, unsigned long long workspace_bytes,
+                                ltxattn_stream_t stream_) {
+  if (!dy || !x || !mean || !rstd || !dx) return LTXATTN_ERR_INVALID_ARG;
+  int st = norm_sizes(rows, cols, groups, dtype);
+  if (st == LTXATTN_ERR_INVALID_ARG) return st;
+  if (dy_stride < cols || x_stride < cols || dx_stride < cols) return LTXATTN_ERR_INVALID_ARG;
+  if (st != LTXATTN_OK) return st;
+  const int item = elem_size(dtype);
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dy) |
+                        reinterpret_cast<uintptr_t>(dx) | reinterpret_cast<uintptr_t>(weight);
+  const uintptr_t mis4 = reinterpret_cast<uintptr_t>(mean) | reinterpret_cast<uintptr_t>(rstd) |
+                         reinterpret_cast<uintptr_t>(dweight) |
+                         reinterpret_cast<uintptr_t>(dbias) |
+                         reinterpret_cast<uintptr_t>(workspace);
+  if ((mis & (uintptr_t)(item - 1)) || (mis4 & 3u)) return LTXATTN_ERR_MISALIGNED;
+  const size_t dx_bytes = norm_bytes(rows, dx_stride, cols, item);
+  const size_t grads = (size_t)groups * cols * 4, stats = (size_t)rows * 4;
+  struct Range {
+    const void* p;
+    size_t n;
+  };
+  const Range in[] = {{dy, norm_bytes(rows, dy_stride, cols, item)},
+                      {x, norm_bytes(rows, x_stride, cols, item)},
+                      {weight, (size_t)groups * cols * item},
+                      {mean, stats},
+                      {rstd, stats}};
+  const bool affine = dweight || dbias;
+  const Range outs[] = {{dx, dx_bytes},
+                        {dweight, grads},
+                        {dbias, grads},
+                        {affine ? workspace : nullptr, (size_t)workspace_bytes}};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i].p) continue;
+    for (int j = 0; j < 5; ++j) {
+      if (!in[j].p) continue;
+      if (i == 0 && j < 2) {
+        if (!norm_alias_ok(dx, dx_stride, in[j].p, j == 0 ? dy_stride : x_stride, rows, cols,
+                           item))
+          return LTXATTN_ERR_INVALID_ARG;
+      } else if (ranges_overlap(outs[i].p, outs[i].n, in[j].p, in[j].n)) {
+        return LTXATTN_ERR_INVALID_ARG;
+      }
+    }
+    for (int j = i + 1; j < 4; ++j)
+      if (outs[j].p && ranges_overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+        return LTXATTN_ERR_INVALID_ARG;
+  }
+  ltx::NormParams p{};
+  p.x = x;
+  p.dy = dy;
+  p.weight = weight;
+  p.out = dx;
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.x_stride = x_stride;
+  p.dy_stride = dy_stride;
+  p.out_stride = dx_stride;
+  p.cols = cols;
+  p.rows_per_group = rows / groups;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  GradPlan plan;
+  st = grad_plan_of(dtype, cols, norm_vector(p, item, true), affine, groups, rows / groups, &plan);
+  if (st != LTXATTN_OK) return st;
+  if (plan.workspace > 0) {
+    if (!workspace || workspace_bytes < plan.workspace) return LTXATTN_ERR_INVALID_ARG;
+    p.partial = static_cast<float*>(workspace);
+  }
+  p.wpr = plan.wpr;
+  p.ctas_per_group = plan.ctas_per_group;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  switch (dtype) {
+    case LTXATTN_BF16: return layer_norm_grad<__nv_bfloat16>(p, groups, affine, plan, stream);
+    case LTXATTN_FP16: return layer_norm_grad<__half>(p, groups, affine, plan, stream);
+    default: return layer_norm_grad<float>(p, groups, affine, plan, stream);
+  }
+}
+
+}  // extern "C"

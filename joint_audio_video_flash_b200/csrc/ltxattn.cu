@@ -22,6 +22,7 @@
 #include "attn_fwd_pair.cuh"
 #include "attn_fwd_pp.cuh"
 #include "attn_fwd_skv.cuh"
+#include "device_context.h"
 #include "na3d_fwd.cuh"
 #include "qk_prologue.cuh"
 
@@ -35,10 +36,7 @@ constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;  // 2 s per wait
 // two-CTAs-per-SM variant of the base kernel
 constexpr int kDualMaxQTiles = 1;
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using ltx::EncodeTiledFn;
 
 struct Workspace {
   void* ptr = nullptr;
@@ -67,6 +65,8 @@ const char* const kEntryPoints[] = {
     "ltxattn_forward_split_noalloc", "ltxattn_qk_norm_rope", "ltxattn_na3d_forward",
     "ltxattn_forward_partial", "ltxattn_combine", "ltxattn_forward_grouped",
     "ltxattn_na3d_plan", "ltxattn_forward_plan",
+    "ltxattn_rope_axes", "ltxattn_layer_norm", "ltxattn_layer_norm_workspace",
+    "ltxattn_layer_norm_backward", "ltxattn_masked_workspace", "ltxattn_masked_forward",
 };
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
@@ -619,6 +619,7 @@ cudaError_t set_smem_limits_all() {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(ltx::ltx_attn_fwd_a2v, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ltx::A2vSmem::kAlloc);
+  if (e == cudaSuccess) e = ltx::masked_set_smem_limits();
   return e;
 }
 
@@ -698,6 +699,18 @@ int forward_one(Context* c, const void* q, const void* k, const void* v, void* o
 }
 
 }  // namespace
+
+namespace ltx {
+
+int device_context(DeviceContext* out) {
+  int st = LTXATTN_OK;
+  const Context* c = current_context(&st);
+  if (!c) return st;
+  *out = DeviceContext{c->encode, c->num_sms, c->d_status};
+  return LTXATTN_OK;
+}
+
+}  // namespace ltx
 
 extern "C" {
 

@@ -1,0 +1,348 @@
+// masked.cu -- host side of attention with masked, capped and distance-biased scores: checks,
+// tensor maps, the plan and the launches of attn_masked_fwd.cuh.
+#include <algorithm>
+#include <cmath>
+
+#include "attn_masked_fwd.cuh"
+#include "combine.cuh"
+#include "device_context.h"
+#include "host_common.h"
+
+namespace {
+
+using ltx::ranges_overlap;
+
+constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per wait
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A [batch, len, heads, head_dim] bf16 tensor with strides in elements; a stride counts only
+// where there is a second row to step to.
+struct Tensor {
+  const void* base;
+  long long batch, len, heads, dim;
+  long long sb, sl, sh;
+};
+
+Tensor make_tensor(const void* base, int batch, int len, int heads, int dim,
+                   const long long* stride) {
+  return Tensor{base,
+                batch,
+                len,
+                heads,
+                dim,
+                batch > 1 ? stride[0] : 0,
+                len > 1 ? stride[1] : 0,
+                heads > 1 ? stride[2] : 0};
+}
+
+size_t tensor_bytes(const Tensor& t) {
+  return 2 * (size_t)((t.batch - 1) * t.sb + (t.len - 1) * t.sl + (t.heads - 1) * t.sh + t.dim);
+}
+
+// No two elements at one address, as the tensor core's tile loads and the stores need it: each
+// axis with a second row has a positive stride (rows of different axes may interleave).
+bool strides_ok(const Tensor& t) {
+  return (t.batch == 1 || t.sb > 0) && (t.len == 1 || t.sl > 0) && (t.heads == 1 || t.sh > 0);
+}
+
+bool aligned16(const Tensor& t) {
+  return ((reinterpret_cast<uintptr_t>(t.base) | (uintptr_t)((t.sb | t.sl | t.sh) * 2)) & 15u) ==
+         0;
+}
+
+// True when the tensors share no byte: their ranges are apart, or they are slices of the same
+// rows (same batch and token strides) whose parts of a row are apart, as the queries, keys and
+// values of one fused projection are.
+bool tensors_apart(const Tensor& a, const Tensor& b) {
+  if (!ranges_overlap(a.base, tensor_bytes(a), b.base, tensor_bytes(b))) return true;
+  const bool rows = a.len == 1 && b.len == 1 && a.batch > 1;  // the batch row is the row
+  const long long row = rows ? a.sb : a.sl;
+  if (row <= 0 || (rows ? b.sb : b.sl) != row) return false;
+  if (!rows && (a.batch > 1 || b.batch > 1) && (a.sb != b.sb || a.sb % row != 0)) return false;
+  const long long bytes = row * 2;
+  const long long wa = ((a.heads - 1) * a.sh + a.dim) * 2, wb = ((b.heads - 1) * b.sh + b.dim) * 2;
+  long long off = (static_cast<const char*>(b.base) - static_cast<const char*>(a.base)) % bytes;
+  if (off < 0) off += bytes;
+  return off >= wa && off + wb <= bytes;
+}
+
+// The tensor as a 4-D TMA tensor (d, head, token, batch); a box is 64 columns of box_heads
+// heads of box_rows tokens, 128-byte swizzled.  Strides of one-row axes only have to be legal.
+bool encode(const ltx::DeviceContext& c, CUtensorMap* map, const Tensor& t, int box_rows,
+            int box_heads) {
+  const cuuint64_t dims[4] = {(cuuint64_t)t.dim, (cuuint64_t)t.heads, (cuuint64_t)t.len,
+                              (cuuint64_t)t.batch};
+  const cuuint64_t row = (cuuint64_t)t.dim * 2;
+  const cuuint64_t strides[3] = {t.sh ? (cuuint64_t)t.sh * 2 : row,
+                                 t.sl ? (cuuint64_t)t.sl * 2 : row,
+                                 t.sb ? (cuuint64_t)t.sb * 2 : row};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapL2promotion promo =
+      t.dim * 2 >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+  return c.encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Tensors {
+  Tensor q, k, v, out;
+};
+
+// Size rules, then what depends on addresses, as the header documents them.
+int check_sizes(const ltxattn_masked_call& a) {
+  if (a.batch < 1 || a.q_len < 1 || a.kv_len < 1 || a.heads < 1 || a.kv_heads < 1 || a.docs < 0)
+    return LTXATTN_ERR_INVALID_ARG;
+  if (a.heads % a.kv_heads != 0) return LTXATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(a.scale) || !(a.scale > 0.0f) || !std::isfinite(a.softcap) ||
+      a.softcap < 0.0f)
+    return LTXATTN_ERR_INVALID_ARG;
+  // a cap so small that scale / cap overflows caps every score to +-cap: not a use
+  if (a.softcap > 0.0f && !std::isfinite(a.scale / a.softcap)) return LTXATTN_ERR_INVALID_ARG;
+  if ((a.docs > 0) != (a.q_starts != nullptr) || (a.docs > 0) != (a.kv_starts != nullptr))
+    return LTXATTN_ERR_INVALID_ARG;
+  if (a.prefix && !a.causal) return LTXATTN_ERR_INVALID_ARG;
+  if (a.head_dim != 64 && a.head_dim != 128) return LTXATTN_ERR_UNSUPPORTED;
+  if (a.q_len > LTXATTN_MAX_LEN || a.kv_len > LTXATTN_MAX_LEN || a.heads > LTXATTN_MAX_HEADS ||
+      a.batch > LTXATTN_MAX_BATCH || a.docs > LTXATTN_MAX_DOCS)
+    return LTXATTN_ERR_UNSUPPORTED;
+  return LTXATTN_OK;
+}
+
+int check_call(const ltxattn_masked_call& a, Tensors* t) {
+  if (!a.q || !a.k || !a.v || !a.out) return LTXATTN_ERR_INVALID_ARG;
+  const int st = check_sizes(a);
+  if (st == LTXATTN_ERR_INVALID_ARG) return st;
+  t->q = make_tensor(a.q, a.batch, a.q_len, a.heads, a.head_dim, a.q_stride);
+  t->k = make_tensor(a.k, a.batch, a.kv_len, a.kv_heads, a.head_dim, a.k_stride);
+  t->v = make_tensor(a.v, a.batch, a.kv_len, a.kv_heads, a.head_dim, a.v_stride);
+  t->out = make_tensor(a.out, a.batch, a.q_len, a.heads, a.head_dim, a.out_stride);
+  for (const Tensor* x : {&t->q, &t->k, &t->v, &t->out})
+    if (!strides_ok(*x)) return LTXATTN_ERR_INVALID_ARG;
+  if (st != LTXATTN_OK) return st;
+  for (const Tensor* x : {&t->q, &t->k, &t->v, &t->out})
+    if (!aligned16(*x)) return LTXATTN_ERR_MISALIGNED;
+  const uintptr_t words =
+      reinterpret_cast<uintptr_t>(a.lse) | reinterpret_cast<uintptr_t>(a.slopes) |
+      reinterpret_cast<uintptr_t>(a.prefix) | reinterpret_cast<uintptr_t>(a.q_starts) |
+      reinterpret_cast<uintptr_t>(a.kv_starts);
+  if (words & 3u) return LTXATTN_ERR_MISALIGNED;
+  return LTXATTN_OK;
+}
+
+// The small device arrays a call reads, and whether [p, p + n) overlaps one of them.
+bool overlaps_small(const ltxattn_masked_call& a, const void* p, size_t n) {
+  const size_t starts = (size_t)a.batch * (a.docs + 1) * 4;
+  return (a.slopes && ranges_overlap(p, n, a.slopes, (size_t)a.heads * 4)) ||
+         (a.prefix && ranges_overlap(p, n, a.prefix, (size_t)a.batch * std::max(a.docs, 1) * 4)) ||
+         (a.q_starts && ranges_overlap(p, n, a.q_starts, starts)) ||
+         (a.kv_starts && ranges_overlap(p, n, a.kv_starts, starts));
+}
+
+size_t lse_bytes(const ltxattn_masked_call& a) {
+  return (size_t)a.batch * a.heads * a.q_len * 4;
+}
+
+ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext& c) {
+  ltx::MaskedShape s{};
+  s.batch = a.batch;
+  s.q_len = a.q_len;
+  s.kv_len = a.kv_len;
+  s.heads = a.heads;
+  s.kv_heads = a.kv_heads;
+  s.group = a.heads / a.kv_heads;
+  s.pack = s.group <= ltx::kBlockM && (s.group & (s.group - 1)) == 0 ? s.group : 1;
+  s.docs = a.docs;
+  s.q_starts = a.q_starts;
+  s.kv_starts = a.kv_starts;
+  s.prefix = a.prefix;
+  s.causal = a.causal ? 1 : 0;
+  s.scale_log2 = a.scale * kLog2e;
+  if (a.softcap > 0.0f) {
+    s.cap_in = a.scale / a.softcap;
+    s.cap_log2 = a.softcap * kLog2e;
+  }
+  s.slopes = a.slopes;
+  s.status = c.d_status;
+  s.timeout_ns = kTimeoutNs;
+  return s;
+}
+
+struct FwdPlan {
+  bool alt;    // one query tile per CTA, accumulators on alternate key tiles
+  int units;   // CTAs along the queries of one (batch row, head): an upper bound
+  int parts;   // key parts
+};
+
+// One tile of queries per document (on average) runs the alternating form: with one tile, the
+// base form's second accumulator would idle.  Key parts as plan_splits in ltxattn.cu counts
+// them: waves of CTAs x (key tiles a part + 4 for the pipeline's fill and the write-out).
+FwdPlan plan_forward(const ltx::MaskedShape& s, int num_sms) {
+  FwdPlan f;
+  const long long docs = std::max(s.docs, 1);
+  f.alt = (long long)s.q_len * s.pack <= docs * ltx::kBlockM;
+  const int rows = ltx::kBlockM / s.pack * (f.alt ? 1 : 2);
+  f.units = (s.q_len + rows - 1) / rows + s.docs;
+  // units that hold rows, as far as the host can tell
+  const long long filled = std::max<long long>((s.q_len + rows - 1) / rows, s.docs);
+  const long long ctas = filled * (s.heads / s.pack) * s.batch;
+  const int tiles = (int)((s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN);
+  f.parts = 1;
+  if (tiles >= 4 && ctas < num_sms) {
+    constexpr int kOverheadTiles = 4;
+    long long best = -1;
+    for (int x = 1; x <= std::min(tiles, 64); ++x) {
+      const long long waves = (ctas * x + num_sms - 1) / num_sms;
+      const long long cost = waves * ((tiles + x - 1) / x + kOverheadTiles);
+      if (best < 0 || cost < best) {
+        best = cost;
+        f.parts = x;
+      }
+    }
+  }
+  return f;
+}
+
+size_t partial_bytes(const ltx::MaskedShape& s, int head_dim, int parts) {
+  return parts > 1 ? (size_t)parts * s.batch * s.heads * s.q_len * (head_dim + 1) * 4 : 0;
+}
+
+template <int D, bool kAlt, bool kCap, bool kBias>
+cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const ltx::MaskedFwdParams& p, int units, cudaStream_t stream) {
+  const dim3 grid((unsigned)units, (unsigned)(p.s.heads / p.s.pack),
+                  (unsigned)(p.s.batch * p.parts));
+  ltx::ltx_masked_fwd<D, kAlt, kCap, kBias>
+      <<<grid, ltx::kMaskedThreads, ltx::MaskedSmem<D, kAlt>::kAlloc, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+template <int D, bool kAlt>
+cudaError_t launch_fwd_scores(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const ltx::MaskedFwdParams& p, int units,
+                              cudaStream_t stream) {
+  if (cap)
+    return bias ? launch_fwd<D, kAlt, true, true>(tq, tk, tv, p, units, stream)
+                : launch_fwd<D, kAlt, true, false>(tq, tk, tv, p, units, stream);
+  return bias ? launch_fwd<D, kAlt, false, true>(tq, tk, tv, p, units, stream)
+              : launch_fwd<D, kAlt, false, false>(tq, tk, tv, p, units, stream);
+}
+
+template <int D>
+cudaError_t launch_forward(const FwdPlan& f, bool cap, bool bias, const CUtensorMap& tq,
+                           const CUtensorMap& tk, const CUtensorMap& tv,
+                           const ltx::MaskedFwdParams& p, cudaStream_t stream) {
+  cudaError_t e = f.alt
+                      ? launch_fwd_scores<D, true>(cap, bias, tq, tk, tv, p, f.units, stream)
+                      : launch_fwd_scores<D, false>(cap, bias, tq, tk, tv, p, f.units, stream);
+  if (e == cudaSuccess && p.parts > 1) {
+    const long long n = (long long)p.s.batch * p.s.heads * p.s.q_len * (D / 4);
+    ltx::ltx_masked_combine<D>
+        <<<(unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads),
+           ltx::kCombineThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+template <int D, bool kAlt, bool kCap, bool kBias>
+cudaError_t set_fwd() {
+  return cudaFuncSetAttribute(ltx::ltx_masked_fwd<D, kAlt, kCap, kBias>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              ltx::MaskedSmem<D, kAlt>::kAlloc);
+}
+
+template <int D, bool kAlt>
+cudaError_t set_fwd_scores() {
+  cudaError_t e = set_fwd<D, kAlt, false, false>();
+  if (e == cudaSuccess) e = set_fwd<D, kAlt, false, true>();
+  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, false>();
+  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, true>();
+  return e;
+}
+
+}  // namespace
+
+namespace ltx {
+
+cudaError_t masked_set_smem_limits() {
+  cudaError_t e = set_fwd_scores<64, false>();
+  if (e == cudaSuccess) e = set_fwd_scores<64, true>();
+  if (e == cudaSuccess) e = set_fwd_scores<128, false>();
+  if (e == cudaSuccess) e = set_fwd_scores<128, true>();
+  return e;
+}
+
+}  // namespace ltx
+
+extern "C" {
+
+int ltxattn_masked_workspace(const ltxattn_masked_call* call, int backward,
+                             unsigned long long* bytes) {
+  if (!call || !bytes) return LTXATTN_ERR_INVALID_ARG;
+  const int st = check_sizes(*call);
+  if (st != LTXATTN_OK) return st;
+  ltx::DeviceContext c;
+  const int err = ltx::device_context(&c);
+  if (err != LTXATTN_OK) return err;
+  const ltx::MaskedShape s = shape_of(*call, c);
+  *bytes = backward ? lse_bytes(*call)
+                    : partial_bytes(s, call->head_dim, plan_forward(s, c.num_sms).parts);
+  return LTXATTN_OK;
+}
+
+int ltxattn_masked_forward(const ltxattn_masked_call* call, void* workspace,
+                           unsigned long long workspace_bytes, ltxattn_stream_t stream_) {
+  if (!call) return LTXATTN_ERR_INVALID_ARG;
+  const ltxattn_masked_call& a = *call;
+  Tensors t;
+  int st = check_call(a, &t);
+  if (st != LTXATTN_OK) return st;
+  for (const Tensor* x : {&t.q, &t.k, &t.v}) {
+    if (!tensors_apart(t.out, *x)) return LTXATTN_ERR_INVALID_ARG;
+    if (a.lse && ranges_overlap(a.lse, lse_bytes(a), x->base, tensor_bytes(*x)))
+      return LTXATTN_ERR_INVALID_ARG;
+  }
+  if (overlaps_small(a, t.out.base, tensor_bytes(t.out)) ||
+      (a.lse && (ranges_overlap(a.lse, lse_bytes(a), t.out.base, tensor_bytes(t.out)) ||
+                 overlaps_small(a, a.lse, lse_bytes(a)))))
+    return LTXATTN_ERR_INVALID_ARG;
+  ltx::DeviceContext c;
+  st = ltx::device_context(&c);
+  if (st != LTXATTN_OK) return st;
+  ltx::MaskedFwdParams p{};
+  p.s = shape_of(a, c);
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.out_stride[0] = t.out.sb;
+  p.out_stride[1] = t.out.sl;
+  p.out_stride[2] = t.out.sh;
+  p.lse = a.lse;
+  const FwdPlan f = plan_forward(p.s, c.num_sms);
+  p.parts = f.parts;
+  if ((long long)a.batch * f.parts > 65535) return LTXATTN_ERR_UNSUPPORTED;
+  const size_t need = partial_bytes(p.s, a.head_dim, f.parts);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return LTXATTN_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(workspace) & 15u) return LTXATTN_ERR_MISALIGNED;
+    for (const Tensor* x : {&t.q, &t.k, &t.v, &t.out})
+      if (ranges_overlap(workspace, need, x->base, tensor_bytes(*x)))
+        return LTXATTN_ERR_INVALID_ARG;
+    if (overlaps_small(a, workspace, need) ||
+        (a.lse && ranges_overlap(workspace, need, a.lse, lse_bytes(a))))
+      return LTXATTN_ERR_INVALID_ARG;
+    p.o_part = static_cast<float*>(workspace);
+    p.lse_part = p.o_part + (size_t)f.parts * a.batch * a.heads * a.q_len * a.head_dim;
+  }
+  CUtensorMap tq, tk, tv;
+  if (!encode(c, &tq, t.q, ltx::kBlockM / p.s.pack, p.s.pack) ||
+      !encode(c, &tk, t.k, ltx::kBlockN, 1) || !encode(c, &tv, t.v, ltx::kBlockN, 1))
+    return LTXATTN_ERR_CUDA;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const bool cap = a.softcap > 0.0f, bias = a.slopes != nullptr;
+  const cudaError_t e = a.head_dim == 64
+                            ? launch_forward<64>(f, cap, bias, tq, tk, tv, p, stream)
+                            : launch_forward<128>(f, cap, bias, tq, tk, tv, p, stream);
+  return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+}
+
+}  // extern "C"

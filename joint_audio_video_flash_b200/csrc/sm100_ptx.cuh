@@ -123,7 +123,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
 
 // Same wait with the polling loop out of line, for the single-thread producer and
 // MMA roles whose hot loops then hold no timer registers.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const WaitCtl ctl) {
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, const WaitCtl ctl) {
   return mbar_wait_poll(bar, parity, ctl);
 }
 
@@ -498,7 +498,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 }
 
 // Polling loop out of line (the single-thread producer and MMA roles).
-__device__ __noinline__ bool mbar_wait_cluster_slow(uint32_t bar, uint32_t parity,
+static __device__ __noinline__ bool mbar_wait_cluster_slow(uint32_t bar, uint32_t parity,
                                                     const WaitCtl ctl) {
   return mbar_wait_cluster_poll(bar, parity, ctl);
 }

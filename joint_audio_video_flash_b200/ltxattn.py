@@ -32,6 +32,30 @@ class LtxAttnError(RuntimeError):
         super().__init__(f"{where}: {status_string(status)} ({status})")
 
 
+class _RopeCall(ctypes.Structure):
+    """``ltxattn_rope_call`` of include/ltxattn.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out")]
+                + [(n, ctypes.c_longlong * 3)
+                   for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+                + [("positions", ctypes.c_void_p), ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+                   ("axis_dims", ctypes.c_int * 4)]
+                + [(n, ctypes.c_int) for n in ("axes", "positions_batch", "batch", "len", "heads",
+                                               "kv_heads", "head_dim", "dtype", "layout",
+                                               "inverse")])
+
+
+class _MaskedCall(ctypes.Structure):
+    """``ltxattn_masked_call`` of include/ltxattn.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse")]
+                + [(n, ctypes.c_longlong * 3)
+                   for n in ("q_stride", "k_stride", "v_stride", "out_stride")]
+                + [(n, ctypes.c_int) for n in ("batch", "q_len", "kv_len", "heads", "kv_heads",
+                                               "head_dim")]
+                + [("scale", ctypes.c_float), ("softcap", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("slopes", "prefix", "q_starts", "kv_starts")]
+                + [("docs", ctypes.c_int), ("causal", ctypes.c_int)])
+
+
 def load() -> ctypes.CDLL:
     """Load libltxattn.so (built by ``joint_audio_video_flash_b200.build``); raise if absent."""
     global _lib
@@ -60,6 +84,15 @@ def load() -> ctypes.CDLL:
             lib.ltxattn_forward_partial.argtypes = [vp, vp, vp, vp, vp] + [ci] * 6 + [cf, vp]
             lib.ltxattn_combine.argtypes = [vp, vp, vp] + [ci] * 5 + [vp]
             lib.ltxattn_forward_grouped.argtypes = [vp, ci, vp]
+            ll, ull = ctypes.c_longlong, ctypes.c_ulonglong
+            lib.ltxattn_rope_axes.argtypes = [ctypes.POINTER(_RopeCall), vp]
+            lib.ltxattn_layer_norm.argtypes = [vp] * 6 + [ll, ci, ll, ll, ll, cf, ci, vp]
+            lib.ltxattn_layer_norm_workspace.argtypes = [ll, ci, ll, ci, ctypes.POINTER(ull)]
+            lib.ltxattn_layer_norm_backward.argtypes = ([vp] * 8 + [ll, ci] + [ll] * 4
+                                                        + [ci, vp, ull, vp])
+            lib.ltxattn_masked_forward.argtypes = [ctypes.POINTER(_MaskedCall), vp, ull, vp]
+            lib.ltxattn_masked_workspace.argtypes = [ctypes.POINTER(_MaskedCall), ci,
+                                                     ctypes.POINTER(ull)]
             lib.ltxattn_entry_point_name.argtypes = [ci]
             lib.ltxattn_entry_point_name.restype = ctypes.c_char_p
             _lib = lib
@@ -394,3 +427,330 @@ def combine(o_parts, lses, q_len: int, out=None, *, stream=None):
         int(head_dim), ctypes.c_void_p(_stream_handle(stream)))
     _check(st, "ltxattn_combine")
     return out
+
+
+# ltxattn_dtype and ltxattn_rope_layout values
+BF16, FP16, FP32 = 0, 1, 2
+ROPE_LAYOUTS = {"pairs": 0, "halves": 1}
+
+
+def _dtype_code(t) -> int:
+    import torch
+    codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+    if t.dtype not in codes:
+        raise TypeError(f"dtype {t.dtype} is none of bfloat16, float16, float32")
+    return codes[t.dtype]
+
+
+def _check_cuda(name: str, t, dtype=None, shape=None, contiguous: bool = False) -> None:
+    """A CUDA tensor on the current device, of this dtype and shape where they are given."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be a {dtype or ''} CUDA tensor".replace("  ", " "))
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_heads(name: str, t, dtype, shape=None) -> None:
+    """A [batch, len, heads, head_dim] CUDA tensor with contiguous channels."""
+    _check_cuda(name, t, dtype, shape)
+    if t.dim() != 4 or 0 in t.shape:
+        raise ValueError(f"{name} must be a non-empty [batch, len, heads, head_dim] tensor")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+
+
+def _strides(t):
+    return (ctypes.c_longlong * 3)(*t.stride()[:3])
+
+
+class _OnStream:
+    """Allocations inside belong to `stream` (torch's allocator reuses their memory in that
+    stream's order), and tensors given to ``used`` are not handed out again before the work
+    queued on it is done."""
+
+    def __init__(self, stream):
+        import torch
+        self.handle = _stream_handle(stream)
+        self.other = stream is not None and self.handle != int(
+            torch.cuda.current_stream().cuda_stream)
+        self.stream = stream
+        self.scope = torch.cuda.stream(stream) if self.other else None
+
+    def __enter__(self):
+        if self.scope is not None:
+            self.scope.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.scope is not None:
+            self.scope.__exit__(*exc)
+        return False
+
+    def used(self, *tensors) -> None:
+        if self.other:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def rope_frequencies(axis_dims, base: float = 10000.0) -> list[float]:
+    """base^(-2i/d) for the pairs i of every axis of d channels, axis after axis: the
+    ``inv_freq`` of :func:`rope_axes` that turns each axis as a one-axis embedding of d
+    channels turns."""
+    return [float(base) ** (-2.0 * i / d) for d in axis_dims for i in range(d // 2)]
+
+
+def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
+              layout: str = "pairs", inverse: bool = False, stream=None):
+    """Rotary positions with several axes (``ltxattn_rope_axes``); returns (q', k').
+
+    q: [B, L, H, D], k: [B, L, Hkv, D] or None (bf16, fp16 or fp32 CUDA, channels contiguous,
+    other strides free); positions: fp32 [B or 1, L, axes]; inv_freq: host numbers, one per
+    rotated pair, axis after axis (see :func:`rope_frequencies`); axis_dims: channels of each
+    axis.  layout "pairs" turns (2i, 2i+1), "halves" (i, i + D/2).  ``inverse`` turns back:
+    the gradient.  The outputs may be the inputs (in place).
+    """
+    import torch
+    code = None
+    for name, t in (("q", q), ("k", k)):
+        if t is None and name == "k":
+            continue
+        _check_heads(name, t, None)
+        code = _dtype_code(t)
+    if k is not None and (k.dtype != q.dtype or k.shape[:2] != q.shape[:2]
+                          or k.shape[3] != q.shape[3]):
+        raise ValueError("k must have q's dtype, batch, length and head_dim")
+    axis_dims = [int(x) for x in axis_dims]
+    inv_freq = [float(x) for x in inv_freq]
+    if not 1 <= len(axis_dims) <= 4:
+        raise ValueError("axis_dims must name one to four axes")
+    if len(inv_freq) != sum(axis_dims) // 2:
+        raise ValueError(f"{len(inv_freq)} frequencies for {sum(axis_dims) // 2} rotated pairs")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    batch, length, heads, head_dim = q.shape
+    _check_cuda("positions", positions, torch.float32, contiguous=True)
+    if positions.dim() != 3 or tuple(positions.shape[1:]) != (length, len(axis_dims)) \
+            or positions.shape[0] not in (1, batch):
+        raise ValueError(f"positions must be [{batch} or 1, {length}, {len(axis_dims)}]")
+    with _OnStream(stream) as on:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        _check_heads("q_out", q_out, q.dtype, q.shape)
+        if k is None:
+            if k_out is not None:
+                raise ValueError("k_out without k")
+        else:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+            _check_heads("k_out", k_out, k.dtype, k.shape)
+        call = _RopeCall(
+            q=_ptr(q), k=_ptr(k), q_out=_ptr(q_out), k_out=_ptr(k_out), q_stride=_strides(q),
+            q_out_stride=_strides(q_out), positions=_ptr(positions),
+            inv_freq=(ctypes.c_double * len(inv_freq))(*inv_freq),
+            axis_dims=(ctypes.c_int * 4)(*axis_dims), axes=len(axis_dims),
+            positions_batch=positions.shape[0], batch=batch, len=length, heads=heads,
+            kv_heads=1 if k is None else k.shape[2], head_dim=head_dim, dtype=code,
+            layout=ROPE_LAYOUTS[layout], inverse=int(bool(inverse)))
+        if k is not None:
+            call.k_stride, call.k_out_stride = _strides(k), _strides(k_out)
+        _check(load().ltxattn_rope_axes(ctypes.byref(call), ctypes.c_void_p(on.handle)),
+               "ltxattn_rope_axes")
+        on.used(q, k, q_out, k_out, positions)
+    return q_out, k_out
+
+
+def _norm_rows(name: str, t, dtype=None, shape=None):
+    """(rows, cols, row stride) of a [..., cols] CUDA tensor whose rows lie at one stride."""
+    _check_cuda(name, t, dtype, shape)
+    if t.dim() < 1 or t.numel() == 0:
+        raise ValueError(f"{name} must be a non-empty [..., cols] tensor")
+    cols = t.shape[-1]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    stride, want = None, None
+    for size, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = step
+        elif step != want:
+            raise ValueError(f"the rows of {name} must lie at one stride")
+        want = step * size
+    return t.numel() // cols, cols, cols if stride is None else stride
+
+
+def _norm_affine(weight, bias, x, rows: int, cols: int) -> int:
+    """Groups of a weight (and bias) of shape [cols] or [groups, cols]."""
+    groups = 1
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        _check_cuda(name, t, x.dtype, contiguous=True)
+        if t.dim() not in (1, 2) or t.shape[-1] != cols:
+            raise ValueError(f"{name} must be [{cols}] or [groups, {cols}]")
+        if name == "bias" and (weight is None or t.shape != weight.shape):
+            raise ValueError("bias must have weight's shape")
+        groups = t.shape[0] if t.dim() == 2 else 1
+    if groups < 1 or rows % groups:
+        raise ValueError(f"{rows} rows do not fall into {groups} equal groups")
+    return groups
+
+
+def layer_norm(x, weight=None, bias=None, out=None, *, eps: float = 1e-6,
+               return_stats: bool = False, stream=None):
+    """Layer norm over the last axis (``ltxattn_layer_norm``); returns out, or (out, mean,
+    rstd) with ``return_stats`` (fp32, one per row: what :func:`layer_norm_backward` reads).
+
+    x: [..., C] (bf16, fp16 or fp32 CUDA; rows at one stride); weight, bias: [C], or [G, C]
+    with one row for each G-th of x's rows in order (the scale and shift of every sample).
+    ``out`` may be x.
+    """
+    import torch
+    rows, cols, x_stride = _norm_rows("x", x)
+    code = _dtype_code(x)
+    groups = _norm_affine(weight, bias, x, rows, cols)
+    with _OnStream(stream) as on:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _, _, out_stride = _norm_rows("out", out, x.dtype, x.shape)
+        mean = rstd = None
+        if return_stats:
+            mean, rstd = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
+        vp = ctypes.c_void_p
+        _check(load().ltxattn_layer_norm(
+            vp(_ptr(x)), vp(_ptr(weight)), vp(_ptr(bias)), vp(_ptr(out)), vp(_ptr(mean)),
+            vp(_ptr(rstd)), rows, cols, groups, x_stride, out_stride, ctypes.c_float(eps), code,
+            vp(on.handle)), "ltxattn_layer_norm")
+        on.used(x, weight, bias, out)
+    return (out, mean, rstd) if return_stats else out
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, *, stream=None):
+    """Gradients of :func:`layer_norm` (``ltxattn_layer_norm_backward``): (dx, dweight, dbias).
+
+    dy: like x; mean, rstd: as the forward call returned them; weight as given to it.
+    dweight and dbias are fp32 of weight's shape, or None without a weight.  ``dx`` may be dy
+    or x.
+    """
+    import torch
+    rows, cols, x_stride = _norm_rows("x", x)
+    code = _dtype_code(x)
+    _, _, dy_stride = _norm_rows("dy", dy, x.dtype, x.shape)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _check_cuda(name, t, torch.float32, x.shape[:-1], contiguous=True)
+    groups = _norm_affine(weight, None, x, rows, cols)
+    lib = load()
+    with _OnStream(stream) as on:
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _, _, dx_stride = _norm_rows("dx", dx, x.dtype, x.shape)
+        dweight = dbias = workspace = None
+        need = ctypes.c_ulonglong(0)
+        if weight is not None:
+            dweight, dbias = torch.empty(2, *weight.shape, dtype=torch.float32, device=x.device)
+            _check(lib.ltxattn_layer_norm_workspace(rows, cols, groups, code,
+                                                    ctypes.byref(need)),
+                   "ltxattn_layer_norm_workspace")
+            if need.value:
+                workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+        vp = ctypes.c_void_p
+        _check(lib.ltxattn_layer_norm_backward(
+            vp(_ptr(dy)), vp(_ptr(x)), vp(_ptr(weight)), vp(_ptr(mean)), vp(_ptr(rstd)),
+            vp(_ptr(dx)), vp(_ptr(dweight)), vp(_ptr(dbias)), rows, cols, groups, dy_stride,
+            x_stride, dx_stride, code, vp(_ptr(workspace)), need.value, vp(on.handle)),
+            "ltxattn_layer_norm_backward")
+        on.used(dy, x, mean, rstd, weight, dx)
+    return dx, dweight, dbias
+
+
+def _masked_call(q, k, v, out, lse, scale, softcap, slopes, causal, prefix, q_starts, kv_starts):
+    """Checks what the library cannot see from raw pointers; returns the filled _MaskedCall."""
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_heads(name, t, torch.bfloat16)
+    batch, q_len, heads, head_dim = q.shape
+    kv_len, kv_heads = k.shape[1:3]
+    if k.shape[0] != batch or k.shape[3] != head_dim or v.shape != k.shape:
+        raise ValueError("k and v must be [batch, kv_len, kv_heads, head_dim] matching q")
+    if (q_starts is None) != (kv_starts is None):
+        raise ValueError("q_starts and kv_starts come together")
+    docs = 0
+    if q_starts is not None:
+        if q_starts.dim() != 2 or q_starts.shape[1] < 2:
+            raise ValueError("q_starts must be [batch, documents + 1]")
+        docs = q_starts.shape[1] - 1
+        for name, t in (("q_starts", q_starts), ("kv_starts", kv_starts)):
+            _check_cuda(name, t, torch.int32, (batch, docs + 1), contiguous=True)
+    if prefix is not None:
+        if not causal:
+            raise ValueError("a prefix needs causal=True (without it every key is visible)")
+        _check_cuda("prefix", prefix, torch.int32, (batch, max(docs, 1)), contiguous=True)
+    if slopes is not None:
+        _check_cuda("slopes", slopes, torch.float32, (heads,), contiguous=True)
+    if out is not None:
+        _check_heads("out", out, torch.bfloat16, q.shape)
+    if lse is not None:
+        _check_cuda("lse", lse, torch.float32, (batch, heads, q_len), contiguous=True)
+    call = _MaskedCall(
+        q=_ptr(q), k=_ptr(k), v=_ptr(v), out=_ptr(out), lse=_ptr(lse), q_stride=_strides(q),
+        k_stride=_strides(k), v_stride=_strides(v), batch=batch, q_len=q_len, kv_len=kv_len,
+        heads=heads, kv_heads=kv_heads, head_dim=head_dim,
+        scale=1.0 / math.sqrt(head_dim) if scale is None else float(scale),
+        softcap=float(softcap), slopes=_ptr(slopes), prefix=_ptr(prefix),
+        q_starts=_ptr(q_starts), kv_starts=_ptr(kv_starts), docs=docs, causal=int(bool(causal)))
+    if out is not None:
+        call.out_stride = _strides(out)
+    return call
+
+
+def _masked_workspace(call, backward: bool, device):
+    import torch
+    need = ctypes.c_ulonglong(0)
+    _check(load().ltxattn_masked_workspace(ctypes.byref(call), int(backward),
+                                           ctypes.byref(need)), "ltxattn_masked_workspace")
+    return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+
+
+def masked_forward(q, k, v, out=None, lse=None, *, scale: float | None = None,
+                   softcap: float = 0.0, slopes=None, causal: bool = False, prefix=None,
+                   q_starts=None, kv_starts=None, stream=None):
+    """Attention with masked, capped and distance-biased scores (``ltxattn_masked_forward``);
+    returns (out, lse), lse fp32 [B, H, Lq] in base 2.
+
+    q: [B, Lq, H, D]; k, v: [B, Lkv, Hkv, D], H a multiple of Hkv (bf16 CUDA, channels
+    contiguous, other strides free).  softcap: s = softcap * tanh(s / softcap).  slopes: fp32
+    [H], subtracts slopes[h] times the token distance.  causal: query i of nq sees the keys up
+    to i + nkv - nq, and the first prefix[b, d] keys (int32 [B, documents or 1]).  q_starts,
+    kv_starts: int32 [B, documents + 1] offsets of packed documents, whose queries see their
+    own document's keys only; rows of no document keep what out and lse held (zeros and -inf
+    when they are allocated here).
+    """
+    import torch
+    call = _masked_call(q, k, v, out, lse, scale, softcap, slopes, causal, prefix, q_starts,
+                        kv_starts)
+    with _OnStream(stream) as on:
+        if out is None:  # rows of no document stay as they are made here
+            make = torch.empty if q_starts is None else torch.zeros
+            out = make(q.shape, dtype=q.dtype, device=q.device)
+            call.out, call.out_stride = _ptr(out), _strides(out)
+        if lse is None:
+            shape = (q.shape[0], q.shape[2], q.shape[1])
+            lse = torch.empty(shape, dtype=torch.float32, device=q.device) if q_starts is None \
+                else torch.full(shape, -math.inf, dtype=torch.float32, device=q.device)
+            call.lse = _ptr(lse)
+        workspace = _masked_workspace(call, False, q.device)
+        _check(load().ltxattn_masked_forward(
+            ctypes.byref(call), ctypes.c_void_p(_ptr(workspace)),
+            0 if workspace is None else workspace.numel(), ctypes.c_void_p(on.handle)),
+            "ltxattn_masked_forward")
+        on.used(q, k, v, out, lse, slopes, prefix, q_starts, kv_starts)
+    return out, lse

@@ -1,0 +1,239 @@
+"""Attention with masked, capped and distance-biased scores against its fp64 definition (needs
+a B200).
+
+Bounds, element by element (oracle/block_ops.py): the output's rounding, P rounded to bf16
+ahead of the PV product, and fp32 scores.
+"""
+import math
+
+import pytest
+import torch
+
+from joint_audio_video_flash_b200 import build, ltxattn
+from oracle import block_ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    build.build()
+    ltxattn.create()
+
+
+def starts(rows):
+    """Offsets from lists of lengths, an optional leading gap as a negative first entry."""
+    out = []
+    for lengths in rows:
+        at = -lengths[0] if lengths[0] < 0 else 0
+        line = [at]
+        for n in lengths[1 if lengths[0] < 0 else 0:]:
+            line.append(line[-1] + n)
+        out.append(line)
+    return torch.tensor(out, dtype=torch.int32)
+
+
+def make(batch, q_len, kv_len, heads, kv_heads, dim, seed=0):
+    g = torch.Generator().manual_seed(seed + q_len + 7 * kv_len)
+
+    def draw(n, h):
+        return torch.randn(batch, n, h, dim, generator=g).bfloat16()
+
+    return draw(q_len, heads), draw(kv_len, kv_heads), draw(kv_len, kv_heads), draw(q_len, heads)
+
+
+def options(heads, cap=0.0, bias=False, scale=None, **kw):
+    slopes = torch.tensor([2.0 ** (-6.0 * (i + 1) / heads) for i in range(heads)]) if bias else None
+    return dict(softcap=cap, slopes=slopes, scale=scale, **kw)
+
+
+def cuda(opts):
+    return {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in opts.items()}
+
+
+def compare(got, ref, names):
+    for n in names:
+        want, err = ref[n], ref[n + "_err"]
+        live = ~torch.isnan(want)
+        g = got[n].cpu().double()
+        same = g == want  # infinities
+        assert torch.all((((g - want).abs() <= err + 1e-30) | same)[live]), \
+            f"{n}: {float(((g - want).abs() / (err + 1e-30))[live & ~same].max())} of the bound"
+
+
+def run(q, k, v, opts):
+    """Forward into marked buffers; rows of no document must keep the marks."""
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((q.shape[0], q.shape[2], q.shape[1]), 5.0, device="cuda")
+    ltxattn.masked_forward(q.cuda(), k.cuda(), v.cuda(), out, lse, **cuda(opts))
+    ltxattn.check()
+    return {"out": out, "lse": lse}
+
+
+FORWARD = [
+    # batch, q_len, kv_len, heads, kv_heads, dim, options
+    (1, 1, 1, 1, 1, 64, {}),
+    (2, 1, 1000, 4, 4, 128, {}),                                   # one query, key parts
+    (2, 1, 1000, 8, 2, 64, dict(causal=True)),
+    (1, 3, 700, 32, 1, 128, dict(causal=True, cap=5.0)),           # 96 packed rows
+    (1, 130, 130, 2, 2, 64, {}),
+    (2, 257, 300, 6, 2, 128, dict(bias=True)),                     # group of 3: not packed
+    (1, 300, 257, 4, 2, 64, dict(causal=True)),                    # early queries see nothing
+    (1, 640, 640, 2, 1, 128, dict(causal=True, cap=8.0, bias=True)),
+    (2, 126, 2000, 2, 2, 64, {}),                                  # one tile, key parts
+    (1, 126, 2000, 2, 2, 128, dict(bias=True, cap=3.0, causal=True)),
+    (1, 33, 129, 3, 3, 128, dict(causal=True, prefix=[[40]])),
+    (2, 500, 500, 4, 1, 64, dict(causal=True, prefix=[[0], [450]])),
+    (1, 200, 200, 2, 2, 64, dict(causal=True, prefix=[[100000]])),  # beyond the keys: all
+    (2, 300, 300, 4, 4, 64, dict(q=[[100, 0, 1, 190], [-5, 128, 129, 0, 20]][:1] * 2)),
+    (2, 300, 310, 4, 2, 128, dict(q=[[-3, 50, 0, 200], [256, 1, 40]],
+                                  kv=[[-1, 60, 30, 129], [0, 130, 180]])),
+    (1, 290, 300, 8, 4, 64, dict(q=[[129, 1, 160]], kv=[[40, 0, 260]], causal=True, bias=True)),
+    (1, 600, 600, 2, 2, 128, dict(q=[[5, 90, 17, 128, 200, 100]], causal=True, cap=4.0,
+                                  prefix=[[2, 95, 0, 60, 30, 1]])),
+    (1, 40, 40, 1, 1, 64, dict(q=[[1] * 40])),                     # forty documents of one
+    (1, 6, 4000, 4, 4, 128, dict(q=[[1, 2, 3]], kv=[[1000, 2500, 500]], causal=True)),
+]
+
+
+@pytest.mark.parametrize("case", FORWARD, ids=lambda c: "-".join(str(x) for x in c))
+def test_forward_matches_definition(case):
+    batch, q_len, kv_len, heads, kv_heads, dim, o = case
+    o = dict(o)
+    qs = o.pop("q", None)
+    if qs is not None:
+        o["q_starts"], o["kv_starts"] = starts(qs), starts(o.pop("kv", qs))
+    if "prefix" in o:
+        o["prefix"] = torch.tensor(o["prefix"], dtype=torch.int32)
+    opts = options(heads, **o)
+    q, k, v, _ = make(batch, q_len, kv_len, heads, kv_heads, dim)
+    ref = block_ops.masked(q, k, v, **opts)
+    got = run(q, k, v, opts)
+    compare(got, ref, ("out", "lse"))
+    outside = torch.isnan(ref["out"])
+    assert torch.all(got["out"].cpu()[outside] == 7)
+    assert torch.all(got["lse"].cpu()[torch.isnan(ref["lse"])] == 5)
+
+
+@pytest.mark.parametrize("dim,q_len", [(64, 1), (64, 200), (128, 90), (128, 300)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_what_is_masked_does_not_reach_a_result(dim, q_len, bad):
+    # every row outside the documents, in q, k and v, is not finite
+    q, k, v, _ = make(1, q_len + 20, 333, 2, 2, dim)
+    opts = dict(q_starts=torch.tensor([[7, 7 + q_len // 2, 7 + q_len]], dtype=torch.int32),
+                kv_starts=torch.tensor([[3, 104, 305]], dtype=torch.int32))
+    ref = block_ops.masked(q, k, v, **opts)
+    q[:, :7], q[:, 7 + q_len:] = bad, bad
+    k[:, :3], k[:, 305:], v[:, :3], v[:, 305:] = bad, bad, bad, bad
+    got = run(q, k, v, opts)
+    compare(got, ref, ("out", "lse"))
+    # and one document's rows do not reach the other's
+    k[:, 104:305], v[:, 104:305] = bad, bad
+    got = run(q, k, v, opts)
+    first = slice(7, 7 + q_len // 2)
+    for n, at in (("out", (slice(None), first)), ("lse", (slice(None), slice(None), first))):
+        want, err = ref[n][at], ref[n + "_err"][at]
+        assert torch.all((got[n].cpu().double()[at] - want).abs() <= err + 1e-30)
+
+
+def test_scores_of_every_size():
+    # weights that underflow, one key that takes all, scores far beyond the cap
+    q, k, v, _ = make(1, 140, 400, 2, 1, 64)
+    for scale, cap in ((30.0, 0.0), (1e-6, 0.0), (30.0, 2.0), (1e4, 50.0), (1e-5, 50.0)):
+        opts = options(2, cap=cap, scale=scale, causal=True)
+        compare(run(q, k, v, opts), block_ops.masked(q, k, v, **opts), ("out", "lse"))
+    # growing scores: the running maximum moves in every key tile
+    k = (k.float() * torch.linspace(0.1, 12, 400)[None, :, None, None]).bfloat16()
+    opts = options(2, scale=1.0)
+    compare(run(q, k, v, opts), block_ops.masked(q, k, v, **opts), ("out", "lse"))
+
+
+def test_strided_views_and_layouts():
+    g = torch.Generator().manual_seed(4)
+    qkv = torch.randn(2, 150, 8 + 2 * 2, 64, generator=g).bfloat16()
+    q, k, v = qkv[:, :, :8], qkv[:, :, 8:10], qkv[:, :, 10:]
+    opts = options(8, causal=True)
+    ref = block_ops.masked(q, k, v, **opts)
+    dev = qkv.cuda()
+    views = dev[:, :, :8], dev[:, :, 8:10], dev[:, :, 10:]
+    out, lse = ltxattn.masked_forward(*views, causal=True)
+    compare({"out": out, "lse": lse}, ref, ("out", "lse"))
+    head_major = [t.transpose(1, 2).contiguous().transpose(1, 2) for t in views]
+    o2 = torch.empty(2, 8, 150, 64, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    ltxattn.masked_forward(*head_major, o2, causal=True)
+    assert torch.equal(o2, out)
+    # the output as a part of the same rows
+    wide = torch.cat([dev, torch.zeros(2, 150, 8, 64, dtype=torch.bfloat16, device="cuda")], 2)
+    ltxattn.masked_forward(wide[:, :, :8], wide[:, :, 8:10], wide[:, :, 10:12], wide[:, :, 12:],
+                           causal=True)
+    assert torch.equal(wide[:, :, 12:], out) and torch.equal(wide[:, :, :12], dev)
+    ltxattn.check()
+
+
+def test_offsets_that_break_the_rules_stay_inside():
+    # the kernel holds every offset inside the tensor; only that is checked here
+    q, k, v, _ = make(1, 100, 100, 2, 2, 64)
+    for line in ([-50, 30, 400], [90, 10, 95], [2 ** 31 - 1, -2 ** 31, 5]):
+        s = torch.tensor([line], dtype=torch.int32)
+        run(q, k, v, dict(q_starts=s, kv_starts=s))
+
+
+def test_streams_and_two_graphs():
+    q, k, v, _ = (t.cuda() for t in make(2, 4, 3000, 4, 4, 64))
+    ref, ref_lse = ltxattn.masked_forward(q, k, v)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = ltxattn.masked_forward(q, k, v, stream=side)
+    side.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    graphs, outs = [], []
+    queries = [q, (q.float() * 2).bfloat16()]
+    for x in queries:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(ltxattn.masked_forward(x, k, v))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    ltxattn.check()
+    for x, (o, l) in zip(queries, outs):
+        want, want_lse = ltxattn.masked_forward(x, k, v)
+        assert torch.equal(o, want) and torch.equal(l, want_lse)
+
+
+def test_refusals():
+    q, k, v, _ = (t.cuda() for t in make(2, 8, 8, 4, 2, 64))
+    s = torch.tensor([[0, 4, 8]] * 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):
+        ltxattn.masked_forward(q.float(), k, v)
+    with pytest.raises(TypeError):
+        ltxattn.masked_forward(q, k, v, q_starts=s.long(), kv_starts=s.long())
+    with pytest.raises(ValueError):
+        ltxattn.masked_forward(q, k, v[:, :4])
+    with pytest.raises(ValueError):
+        ltxattn.masked_forward(q, k, v, q_starts=s)
+    with pytest.raises(ValueError):
+        ltxattn.masked_forward(q, k, v, prefix=torch.zeros(2, 1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        ltxattn.masked_forward(q, k, v, slopes=torch.zeros(2, device="cuda"))
+    for status, call in (
+            (ltxattn.ERR_INVALID_ARG, lambda: ltxattn.masked_forward(q[:, :, :3], k, v)),
+            (ltxattn.ERR_INVALID_ARG, lambda: ltxattn.masked_forward(q, k, v, q)),
+            (ltxattn.ERR_INVALID_ARG, lambda: ltxattn.masked_forward(q, k, v, softcap=-1.0)),
+            (ltxattn.ERR_INVALID_ARG, lambda: ltxattn.masked_forward(q, k, v, scale=math.nan)),
+            (ltxattn.ERR_INVALID_ARG,
+             lambda: ltxattn.masked_forward(q, k[:1].expand(2, 8, 2, 64), v)),
+            (ltxattn.ERR_UNSUPPORTED,
+             lambda: ltxattn.masked_forward(*(t[..., :32].contiguous() for t in (q, k, v)))),
+            (ltxattn.ERR_MISALIGNED, lambda: ltxattn.masked_forward(
+                torch.zeros(2, 8, 4, 68, dtype=torch.bfloat16, device="cuda")[..., :64], k, v))):
+        with pytest.raises(ltxattn.LtxAttnError) as e:
+            call()
+        assert e.value.status == status
