@@ -518,6 +518,41 @@ LTXATTN_API int ltxattn_masked_forward(const ltxattn_masked_call* call, void* wo
                                        unsigned long long workspace_bytes,
                                        ltxattn_stream_t stream);
 
+/* Gradients of ltxattn_masked_backward: bf16, shaped and strided as the tensors they belong to
+ * (strides of their own). */
+typedef struct ltxattn_masked_grad {
+  const void* d_out;
+  void* dq;
+  void* dk;
+  void* dv;
+  long long d_out_stride[3]; /* elements between batch rows, tokens, heads */
+  long long dq_stride[3];
+  long long dk_stride[3];
+  long long dv_stride[3];
+} ltxattn_masked_grad;
+
+/*
+ * Gradients of ltxattn_masked_forward: with P = softmax(s), t = tanh(scale q.k / softcap)
+ * (t = 0 without a cap) and delta_i = d_out_i . out_i
+ *     dv_j = sum_i P_ij d_out_i
+ *     dS_ij = P_ij (d_out_i . v_j - delta_i) (1 - t_ij^2)
+ *     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i
+ * summed over the query heads of a key head.  `call` as given to the forward call, out and lse
+ * as it wrote them (lse required); the slopes get no gradient.  Queries that see no key have
+ * gradient 0, keys that no query sees too; rows of no document are left as they were.  dq, dk
+ * and dv must share no byte with each other, with a tensor of `call` or d_out.
+ *
+ *   workspace  device, 16-byte aligned, at least what ltxattn_masked_workspace(call, 1) says;
+ *              calls that may overlap in time need one each.
+ * bf16 products with P and dS rounded to bf16 ahead of theirs, everything else fp32, each
+ * gradient rounded once.  Sums run in a fixed order (the same call gives the same bits).
+ * Needs ltxattn_create; checks and errors as ltxattn_masked_forward.
+ */
+LTXATTN_API int ltxattn_masked_backward(const ltxattn_masked_call* call,
+                                        const ltxattn_masked_grad* grad, void* workspace,
+                                        unsigned long long workspace_bytes,
+                                        ltxattn_stream_t stream);
+
 /*
  * Bytes of device workspace the masked call needs on the current device (backward != 0: the
  * backward call).  Sizes, docs and causal are read; pointers only for being NULL or not.

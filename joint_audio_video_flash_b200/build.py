@@ -13,7 +13,7 @@ SOURCES = ["ltxattn.cu", "masked.cu", "block_ops.cu"]
 DEPS = ["ltxattn.cu", "attn_fwd.cuh", "attn_fwd_pp.cuh", "attn_fwd_skv.cuh", "attn_fwd_pair.cuh",
         "attn_fwd_a2v.cuh", "qk_prologue.cuh",
         "na3d_fwd.cuh", "combine.cuh", "debug_guard.cuh", "sm100_ptx.cuh", "masked.cu",
-        "attn_masked_fwd.cuh", "block_ops.cu", "rope_axes.cuh", "layer_norm.cuh", "dtype.cuh",
+        "attn_masked_fwd.cuh", "attn_masked_bwd.cuh", "block_ops.cu", "rope_axes.cuh", "layer_norm.cuh", "dtype.cuh",
         "device_context.h", "host_common.h"]
 NVCC_FLAGS = ["--threads", "0",  # the sources compile side by side
               "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",

@@ -67,6 +67,7 @@ const char* const kEntryPoints[] = {
     "ltxattn_na3d_plan", "ltxattn_forward_plan",
     "ltxattn_rope_axes", "ltxattn_layer_norm", "ltxattn_layer_norm_workspace",
     "ltxattn_layer_norm_backward", "ltxattn_masked_workspace", "ltxattn_masked_forward",
+    "ltxattn_masked_backward",
 };
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {

@@ -1,8 +1,9 @@
 // masked.cu -- host side of attention with masked, capped and distance-biased scores: checks,
-// tensor maps, the plan and the launches of attn_masked_fwd.cuh.
+// tensor maps, the plan and the launches of attn_masked_fwd.cuh and attn_masked_bwd.cuh.
 #include <algorithm>
 #include <cmath>
 
+#include "attn_masked_bwd.cuh"
 #include "attn_masked_fwd.cuh"
 #include "combine.cuh"
 #include "device_context.h"
@@ -174,9 +175,25 @@ struct FwdPlan {
   int parts;   // key parts
 };
 
+// Parts of a walk of `steps` tiles by each of `ctas` CTAs, as plan_splits in ltxattn.cu counts
+// them: waves of CTAs x (steps a part + `fixed` for the pipeline's fill and the write-out).
+int plan_parts(long long ctas, long long steps, int num_sms, int fixed) {
+  if (steps < 4 || ctas >= num_sms) return 1;
+  int parts = 1;
+  long long best = -1;
+  for (int x = 1; x <= (int)std::min<long long>(steps, 64); ++x) {
+    const long long waves = (ctas * x + num_sms - 1) / num_sms;
+    const long long cost = waves * ((steps + x - 1) / x + fixed);
+    if (best < 0 || cost < best) {
+      best = cost;
+      parts = x;
+    }
+  }
+  return parts;
+}
+
 // One tile of queries per document (on average) runs the alternating form: with one tile, the
-// base form's second accumulator would idle.  Key parts as plan_splits in ltxattn.cu counts
-// them: waves of CTAs x (key tiles a part + 4 for the pipeline's fill and the write-out).
+// base form's second accumulator would idle.
 FwdPlan plan_forward(const ltx::MaskedShape& s, int num_sms) {
   FwdPlan f;
   const long long docs = std::max(s.docs, 1);
@@ -186,20 +203,8 @@ FwdPlan plan_forward(const ltx::MaskedShape& s, int num_sms) {
   // units that hold rows, as far as the host can tell
   const long long filled = std::max<long long>((s.q_len + rows - 1) / rows, s.docs);
   const long long ctas = filled * (s.heads / s.pack) * s.batch;
-  const int tiles = (int)((s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN);
-  f.parts = 1;
-  if (tiles >= 4 && ctas < num_sms) {
-    constexpr int kOverheadTiles = 4;
-    long long best = -1;
-    for (int x = 1; x <= std::min(tiles, 64); ++x) {
-      const long long waves = (ctas * x + num_sms - 1) / num_sms;
-      const long long cost = waves * ((tiles + x - 1) / x + kOverheadTiles);
-      if (best < 0 || cost < best) {
-        best = cost;
-        f.parts = x;
-      }
-    }
-  }
+  const long long tiles = (s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN;
+  f.parts = plan_parts(ctas, tiles, num_sms, 4);
   return f;
 }
 
@@ -245,6 +250,143 @@ cudaError_t launch_forward(const FwdPlan& f, bool cap, bool bias, const CUtensor
   return e;
 }
 
+// ---------------------------------------------------------------- backward
+struct BwdPlan {
+  int units_kv, units_q;  // CTAs along the keys, the queries: upper bounds
+  int parts_kv, parts_q;
+  size_t stat, partials;  // bytes of workspace
+};
+
+BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, int num_sms) {
+  BwdPlan f;
+  const long long docs = std::max(s.docs, 1);
+  const int kt = (s.kv_len + ltx::kBlockN - 1) / ltx::kBlockN;
+  const int qt = (s.q_len + ltx::kBlockM - 1) / ltx::kBlockM;
+  f.units_kv = kt + s.docs;
+  f.units_q = qt + s.docs;
+  const long long q_steps = (s.q_len / docs + ltx::kBlockM - 1) / ltx::kBlockM;
+  const long long kv_steps = (s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN;
+  f.parts_kv = plan_parts(std::max<long long>(kt, s.docs) * s.kv_heads * s.batch,
+                          q_steps * s.group, num_sms, 4);
+  f.parts_q = plan_parts(std::max<long long>(qt, s.docs) * s.heads * s.batch, kv_steps, num_sms,
+                         4);
+  f.stat = ((size_t)s.batch * s.heads * s.q_len * sizeof(float2) + 15) / 16 * 16;
+  const size_t row = (size_t)head_dim * sizeof(float);
+  const size_t kv = f.parts_kv > 1
+                        ? 2 * (size_t)f.parts_kv * s.batch * s.kv_heads * s.kv_len * row : 0;
+  const size_t q = f.parts_q > 1 ? (size_t)f.parts_q * s.batch * s.heads * s.q_len * row : 0;
+  f.partials = std::max(kv, q);  // used one after the other
+  return f;
+}
+
+struct BwdMaps {
+  CUtensorMap q, k, v, d_out;
+};
+
+template <int D, bool kCap, bool kBias>
+cudaError_t launch_kv(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
+                      cudaStream_t stream) {
+  const dim3 grid((unsigned)units, (unsigned)p.s.kv_heads, (unsigned)(p.s.batch * p.parts));
+  ltx::ltx_masked_bwd_kv<D, kCap, kBias>
+      <<<grid, ltx::kMaskedThreads, ltx::BwdKvSmem<D>::kAlloc, stream>>>(t.q, t.k, t.v, t.d_out,
+                                                                         p);
+  return cudaGetLastError();
+}
+
+template <int D, bool kCap, bool kBias>
+cudaError_t launch_q(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
+                     cudaStream_t stream) {
+  const dim3 grid((unsigned)units, (unsigned)p.s.heads, (unsigned)(p.s.batch * p.parts));
+  ltx::ltx_masked_bwd_q<D, kCap, kBias>
+      <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D>::kAlloc, stream>>>(t.q, t.k, t.v, t.d_out, p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_sum(const float* part, const Tensor& out, int parts, const int* starts,
+                       int docs, cudaStream_t stream) {
+  const long long n = out.batch * out.heads * out.len * (D / 4);
+  ltx::ltx_masked_bwd_sum<D>
+      <<<(unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads), ltx::kCombineThreads,
+         0, stream>>>(part, static_cast<__nv_bfloat16*>(const_cast<void*>(out.base)), parts,
+                      (int)out.batch, (int)out.heads, (int)out.len, starts, docs, out.sb, out.sl,
+                      out.sh);
+  return cudaGetLastError();
+}
+
+void set_target(const Tensor& t, __nv_bfloat16** base, long long* stride) {
+  *base = static_cast<__nv_bfloat16*>(const_cast<void*>(t.base));
+  stride[0] = t.sb;
+  stride[1] = t.sl;
+  stride[2] = t.sh;
+}
+
+template <int D>
+cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, const Tensors& t,
+                            const Tensor& d_out, const Tensor& dq, const Tensor& dk,
+                            const Tensor& dv, const BwdMaps& maps, ltx::MaskedBwdParams p,
+                            float* partials, cudaStream_t stream) {
+  ltx::ltx_masked_stat<D>
+      <<<dim3((unsigned)((a.q_len + ltx::kStatTokens - 1) / ltx::kStatTokens), (unsigned)a.heads,
+              (unsigned)a.batch),
+         256, 0, stream>>>(static_cast<const __nv_bfloat16*>(t.out.base),
+                           static_cast<const __nv_bfloat16*>(d_out.base), a.lse,
+                           const_cast<float2*>(p.stat), a.heads, a.q_len, t.out.sb, t.out.sl,
+                           t.out.sh, d_out.sb, d_out.sl, d_out.sh);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool cap = a.softcap > 0.0f, bias = a.slopes != nullptr;
+  // dK and dV
+  p.parts = f.parts_kv;
+  set_target(dk, &p.d0, p.stride0);
+  set_target(dv, &p.d1, p.stride1);
+  if (p.parts > 1) {
+    p.part0 = partials;
+    p.part1 = partials + (size_t)p.parts * a.batch * a.kv_heads * a.kv_len * D;
+  }
+  e = cap ? (bias ? launch_kv<D, true, true>(maps, p, f.units_kv, stream)
+                  : launch_kv<D, true, false>(maps, p, f.units_kv, stream))
+          : (bias ? launch_kv<D, false, true>(maps, p, f.units_kv, stream)
+                  : launch_kv<D, false, false>(maps, p, f.units_kv, stream));
+  if (e == cudaSuccess && p.parts > 1) {
+    e = launch_sum<D>(p.part0, dk, p.parts, a.kv_starts, a.docs, stream);
+    if (e == cudaSuccess) e = launch_sum<D>(p.part1, dv, p.parts, a.kv_starts, a.docs, stream);
+  }
+  if (e != cudaSuccess) return e;
+  // dQ
+  p.parts = f.parts_q;
+  set_target(dq, &p.d0, p.stride0);
+  p.part0 = p.parts > 1 ? partials : nullptr;
+  p.part1 = nullptr;
+  e = cap ? (bias ? launch_q<D, true, true>(maps, p, f.units_q, stream)
+                  : launch_q<D, true, false>(maps, p, f.units_q, stream))
+          : (bias ? launch_q<D, false, true>(maps, p, f.units_q, stream)
+                  : launch_q<D, false, false>(maps, p, f.units_q, stream));
+  if (e == cudaSuccess && p.parts > 1)
+    e = launch_sum<D>(p.part0, dq, p.parts, a.q_starts, a.docs, stream);
+  return e;
+}
+
+template <int D, bool kCap, bool kBias>
+cudaError_t set_bwd() {
+  cudaError_t e = cudaFuncSetAttribute(ltx::ltx_masked_bwd_kv<D, kCap, kBias>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       ltx::BwdKvSmem<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, kCap, kBias>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              ltx::BwdQSmem<D>::kAlloc);
+}
+
+template <int D>
+cudaError_t set_bwd_scores() {
+  cudaError_t e = set_bwd<D, false, false>();
+  if (e == cudaSuccess) e = set_bwd<D, false, true>();
+  if (e == cudaSuccess) e = set_bwd<D, true, false>();
+  if (e == cudaSuccess) e = set_bwd<D, true, true>();
+  return e;
+}
+
 template <int D, bool kAlt, bool kCap, bool kBias>
 cudaError_t set_fwd() {
   return cudaFuncSetAttribute(ltx::ltx_masked_fwd<D, kAlt, kCap, kBias>,
@@ -270,6 +412,8 @@ cudaError_t masked_set_smem_limits() {
   if (e == cudaSuccess) e = set_fwd_scores<64, true>();
   if (e == cudaSuccess) e = set_fwd_scores<128, false>();
   if (e == cudaSuccess) e = set_fwd_scores<128, true>();
+  if (e == cudaSuccess) e = set_bwd_scores<64>();
+  if (e == cudaSuccess) e = set_bwd_scores<128>();
   return e;
 }
 
@@ -286,8 +430,12 @@ int ltxattn_masked_workspace(const ltxattn_masked_call* call, int backward,
   const int err = ltx::device_context(&c);
   if (err != LTXATTN_OK) return err;
   const ltx::MaskedShape s = shape_of(*call, c);
-  *bytes = backward ? lse_bytes(*call)
-                    : partial_bytes(s, call->head_dim, plan_forward(s, c.num_sms).parts);
+  if (backward) {
+    const BwdPlan f = plan_backward(s, call->head_dim, c.num_sms);
+    *bytes = f.stat + f.partials;
+  } else {
+    *bytes = partial_bytes(s, call->head_dim, plan_forward(s, c.num_sms).parts);
+  }
   return LTXATTN_OK;
 }
 
@@ -342,6 +490,70 @@ int ltxattn_masked_forward(const ltxattn_masked_call* call, void* workspace,
   const cudaError_t e = a.head_dim == 64
                             ? launch_forward<64>(f, cap, bias, tq, tk, tv, p, stream)
                             : launch_forward<128>(f, cap, bias, tq, tk, tv, p, stream);
+  return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+}
+
+int ltxattn_masked_backward(const ltxattn_masked_call* call, const ltxattn_masked_grad* grad,
+                            void* workspace, unsigned long long workspace_bytes,
+                            ltxattn_stream_t stream_) {
+  if (!call || !grad) return LTXATTN_ERR_INVALID_ARG;
+  const ltxattn_masked_call& a = *call;
+  const ltxattn_masked_grad& g = *grad;
+  if (!g.d_out || !g.dq || !g.dk || !g.dv || !a.lse) return LTXATTN_ERR_INVALID_ARG;
+  Tensors t;
+  int st = check_call(a, &t);
+  if (st == LTXATTN_ERR_INVALID_ARG) return st;
+  const int d = a.head_dim;
+  const Tensor d_out = make_tensor(g.d_out, a.batch, a.q_len, a.heads, d, g.d_out_stride);
+  const Tensor dq = make_tensor(g.dq, a.batch, a.q_len, a.heads, d, g.dq_stride);
+  const Tensor dk = make_tensor(g.dk, a.batch, a.kv_len, a.kv_heads, d, g.dk_stride);
+  const Tensor dv = make_tensor(g.dv, a.batch, a.kv_len, a.kv_heads, d, g.dv_stride);
+  for (const Tensor* x : {&d_out, &dq, &dk, &dv})
+    if (!strides_ok(*x)) return LTXATTN_ERR_INVALID_ARG;
+  if (st != LTXATTN_OK) return st;
+  for (const Tensor* x : {&d_out, &dq, &dk, &dv})
+    if (!aligned16(*x)) return LTXATTN_ERR_MISALIGNED;
+  const Tensor* const in[] = {&t.q, &t.k, &t.v, &t.out, &d_out};
+  const Tensor* const outs[] = {&dq, &dk, &dv};
+  for (int i = 0; i < 3; ++i) {
+    for (const Tensor* x : in)
+      if (!tensors_apart(*outs[i], *x)) return LTXATTN_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 3; ++j)
+      if (!tensors_apart(*outs[i], *outs[j])) return LTXATTN_ERR_INVALID_ARG;
+    const size_t n = tensor_bytes(*outs[i]);
+    if (ranges_overlap(outs[i]->base, n, a.lse, lse_bytes(a)) ||
+        overlaps_small(a, outs[i]->base, n))
+      return LTXATTN_ERR_INVALID_ARG;
+  }
+  ltx::DeviceContext c;
+  st = ltx::device_context(&c);
+  if (st != LTXATTN_OK) return st;
+  ltx::MaskedBwdParams p{};
+  p.s = shape_of(a, c);
+  p.s.pack = 1;
+  p.scale = a.scale;
+  const BwdPlan f = plan_backward(p.s, d, c.num_sms);
+  if ((long long)a.batch * std::max(f.parts_kv, f.parts_q) > 65535) return LTXATTN_ERR_UNSUPPORTED;
+  const size_t need = f.stat + f.partials;
+  if (!workspace || workspace_bytes < need) return LTXATTN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & 15u) return LTXATTN_ERR_MISALIGNED;
+  for (const Tensor* x : in)
+    if (ranges_overlap(workspace, need, x->base, tensor_bytes(*x))) return LTXATTN_ERR_INVALID_ARG;
+  for (const Tensor* x : outs)
+    if (ranges_overlap(workspace, need, x->base, tensor_bytes(*x))) return LTXATTN_ERR_INVALID_ARG;
+  if (overlaps_small(a, workspace, need) ||
+      ranges_overlap(workspace, need, a.lse, lse_bytes(a)))
+    return LTXATTN_ERR_INVALID_ARG;
+  p.stat = static_cast<const float2*>(workspace);
+  float* partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + f.stat);
+  BwdMaps maps;
+  if (!encode(c, &maps.q, t.q, ltx::kBlockM, 1) || !encode(c, &maps.k, t.k, ltx::kBlockN, 1) ||
+      !encode(c, &maps.v, t.v, ltx::kBlockN, 1) || !encode(c, &maps.d_out, d_out, ltx::kBlockM, 1))
+    return LTXATTN_ERR_CUDA;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const cudaError_t e =
+      d == 64 ? launch_backward<64>(f, a, t, d_out, dq, dk, dv, maps, p, partials, stream)
+              : launch_backward<128>(f, a, t, d_out, dq, dk, dv, maps, p, partials, stream);
   return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
 }
 

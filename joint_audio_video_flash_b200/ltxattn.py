@@ -56,6 +56,13 @@ class _MaskedCall(ctypes.Structure):
                 + [("docs", ctypes.c_int), ("causal", ctypes.c_int)])
 
 
+class _MaskedGrad(ctypes.Structure):
+    """``ltxattn_masked_grad`` of include/ltxattn.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("d_out", "dq", "dk", "dv")]
+                + [(n, ctypes.c_longlong * 3)
+                   for n in ("d_out_stride", "dq_stride", "dk_stride", "dv_stride")])
+
+
 def load() -> ctypes.CDLL:
     """Load libltxattn.so (built by ``joint_audio_video_flash_b200.build``); raise if absent."""
     global _lib
@@ -91,6 +98,8 @@ def load() -> ctypes.CDLL:
             lib.ltxattn_layer_norm_backward.argtypes = ([vp] * 8 + [ll, ci] + [ll] * 4
                                                         + [ci, vp, ull, vp])
             lib.ltxattn_masked_forward.argtypes = [ctypes.POINTER(_MaskedCall), vp, ull, vp]
+            lib.ltxattn_masked_backward.argtypes = [ctypes.POINTER(_MaskedCall),
+                                                    ctypes.POINTER(_MaskedGrad), vp, ull, vp]
             lib.ltxattn_masked_workspace.argtypes = [ctypes.POINTER(_MaskedCall), ci,
                                                      ctypes.POINTER(ull)]
             lib.ltxattn_entry_point_name.argtypes = [ci]
@@ -754,3 +763,38 @@ def masked_forward(q, k, v, out=None, lse=None, *, scale: float | None = None,
             "ltxattn_masked_forward")
         on.used(q, k, v, out, lse, slopes, prefix, q_starts, kv_starts)
     return out, lse
+
+
+def masked_backward(d_out, q, k, v, out, lse, dq=None, dk=None, dv=None, *,
+                    scale: float | None = None, softcap: float = 0.0, slopes=None,
+                    causal: bool = False, prefix=None, q_starts=None, kv_starts=None,
+                    stream=None):
+    """Gradients of :func:`masked_forward` (``ltxattn_masked_backward``): (dq, dk, dv), bf16.
+
+    d_out: like q; out, lse: what the forward call returned; the options as given to it.  Rows
+    of no document keep what dq, dk and dv held (zeros when they are allocated here).
+    """
+    import torch
+    call = _masked_call(q, k, v, out, lse, scale, softcap, slopes, causal, prefix, q_starts,
+                        kv_starts)
+    if out is None or lse is None:
+        raise ValueError("out and lse of the forward call are needed")
+    _check_heads("d_out", d_out, torch.bfloat16, q.shape)
+    with _OnStream(stream) as on:
+        make = torch.empty if q_starts is None else torch.zeros
+        grads = []
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            if t is None:
+                t = make(like.shape, dtype=like.dtype, device=like.device)
+            _check_heads(name, t, torch.bfloat16, like.shape)
+            grads.append(t)
+        dq, dk, dv = grads
+        grad = _MaskedGrad(d_out=_ptr(d_out), dq=_ptr(dq), dk=_ptr(dk), dv=_ptr(dv),
+                           d_out_stride=_strides(d_out), dq_stride=_strides(dq),
+                           dk_stride=_strides(dk), dv_stride=_strides(dv))
+        workspace = _masked_workspace(call, True, q.device)
+        _check(load().ltxattn_masked_backward(
+            ctypes.byref(call), ctypes.byref(grad), ctypes.c_void_p(_ptr(workspace)),
+            workspace.numel(), ctypes.c_void_p(on.handle)), "ltxattn_masked_backward")
+        on.used(d_out, q, k, v, out, lse, dq, dk, dv, slopes, prefix, q_starts, kv_starts)
+    return dq, dk, dv

@@ -117,6 +117,136 @@ def test_forward_matches_definition(case):
     assert torch.all(got["lse"].cpu()[torch.isnan(ref["lse"])] == 5)
 
 
+BACKWARD = [
+    # batch, q_len, kv_len, heads, kv_heads, dim, options
+    (1, 1, 1, 1, 1, 64, {}),
+    (2, 5, 7, 2, 1, 128, dict(causal=True)),
+    (1, 130, 130, 2, 2, 64, {}),
+    (2, 257, 300, 6, 2, 128, dict(bias=True)),
+    (1, 300, 257, 4, 2, 64, dict(causal=True)),                     # queries that see nothing
+    (1, 257, 600, 2, 2, 128, dict(causal=True, cap=6.0)),
+    (1, 640, 640, 2, 1, 128, dict(causal=True, cap=8.0, bias=True)),
+    (1, 126, 2000, 2, 2, 64, dict(cap=4.0)),                        # dq in key parts
+    (1, 2000, 126, 2, 1, 128, {}),                                  # dk, dv in query parts
+    (2, 500, 500, 4, 1, 64, dict(causal=True, prefix=[[0], [450]])),
+    (1, 33, 129, 3, 3, 128, dict(causal=True, prefix=[[40]], bias=True)),
+    (2, 300, 310, 4, 2, 128, dict(q=[[-3, 50, 0, 200], [256, 1, 40]],
+                                  kv=[[-1, 60, 30, 129], [0, 130, 180]])),
+    (1, 290, 300, 8, 4, 64, dict(q=[[129, 1, 160]], kv=[[40, 0, 260]], causal=True, bias=True)),
+    (1, 600, 600, 2, 2, 128, dict(q=[[5, 90, 17, 128, 200, 100]], causal=True, cap=4.0,
+                                  prefix=[[2, 95, 0, 60, 30, 1]])),
+    (1, 700, 2100, 2, 2, 64, dict(q=[[300, 400]], kv=[[1000, 1100]], causal=True)),
+]
+
+
+def run_backward(q, k, v, d_out, opts):
+    """Forward and backward into marked buffers."""
+    opts = cuda(opts)
+    q, k, v, d_out = (t.cuda() for t in (q, k, v, d_out))
+    out, lse = ltxattn.masked_forward(q, k, v, **opts)
+    marked = [torch.full(t.shape, 7.0, dtype=torch.bfloat16, device="cuda") for t in (q, k, v)]
+    ltxattn.masked_backward(d_out, q, k, v, out, lse, *marked, **opts)
+    ltxattn.check()
+    return dict(zip(("dq", "dk", "dv"), marked))
+
+
+def covered(off, b, length):
+    at = torch.zeros(length, dtype=torch.bool)
+    at[0 if off is None else int(off[b, 0]):length if off is None else int(off[b, -1])] = True
+    return at
+
+
+@pytest.mark.parametrize("case", BACKWARD, ids=lambda c: "-".join(str(x) for x in c))
+def test_backward_matches_definition(case):
+    batch, q_len, kv_len, heads, kv_heads, dim, o = case
+    o = dict(o)
+    qs = o.pop("q", None)
+    if qs is not None:
+        o["q_starts"], o["kv_starts"] = starts(qs), starts(o.pop("kv", qs))
+    if "prefix" in o:
+        o["prefix"] = torch.tensor(o["prefix"], dtype=torch.int32)
+    opts = options(heads, **o)
+    q, k, v, d_out = make(batch, q_len, kv_len, heads, kv_heads, dim)
+    ref = block_ops.masked(q, k, v, d_out=d_out, **opts)
+    got = run_backward(q, k, v, d_out, opts)
+    for b in range(batch):
+        for n, off, length in (("dq", opts.get("q_starts"), q_len),
+                               ("dk", opts.get("kv_starts"), kv_len),
+                               ("dv", opts.get("kv_starts"), kv_len)):
+            inside = covered(off, b, length)
+            assert torch.all(got[n][b].cpu()[~inside] == 7), n
+            compare({n: got[n][b].cpu()[inside]},
+                    {n: ref[n][b][inside], n + "_err": ref[n + "_err"][b][inside]}, (n,))
+            # and as a whole: P, dS and the result are rounded, three independent errors of
+            # 2^-8 / sqrt(3) rms at most; delta's own error adds as much again
+            diff = got[n][b].cpu().double()[inside] - ref[n][b][inside]
+            norm = float(ref[n][b][inside].norm())
+            assert float(diff.norm()) <= 2 ** -7 * norm + 1e-6, n
+    again = run_backward(q, k, v, d_out, opts)
+    assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_gradients_against_differences(dim):
+    # a directional difference of the definition's loss: the gradients are within their bf16
+    # rounding of it
+    q, k, v, d_out = make(1, 40, 50, 2, 1, dim, seed=9)
+    opts = options(2, cap=3.0, bias=True, causal=True)
+    got = run_backward(q, k, v, d_out, opts)
+    g = torch.Generator().manual_seed(1)
+
+    def loss(*qkv):
+        return float((block_ops.masked(*qkv, **opts)["out"] * d_out.double()).sum())
+
+    for at, n in enumerate(("dq", "dk", "dv")):
+        x = [q.double(), k.double(), v.double()]
+        direction = torch.randn(x[at].shape, generator=g).double()
+        h = 1e-4
+        up, down = list(x), list(x)
+        up[at], down[at] = x[at] + h * direction, x[at] - h * direction
+        diff = (loss(*up) - loss(*down)) / (2 * h)
+        terms = got[n].cpu().double() * direction
+        # every element off by 2^-6 of itself at most on average (rounded three times)
+        assert abs(float(terms.sum()) - diff) <= 2 ** -6 * float(terms.abs().sum())
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_masked_rows_do_not_reach_a_gradient(bad):
+    q, k, v, d_out = make(1, 170, 333, 2, 1, 64)
+    opts = dict(q_starts=torch.tensor([[7, 90, 161]], dtype=torch.int32),
+                kv_starts=torch.tensor([[3, 104, 305]], dtype=torch.int32))
+    ref = block_ops.masked(q, k, v, d_out=d_out, **opts)
+    for t in (q, d_out):
+        t[:, :7], t[:, 161:] = bad, bad
+    for t in (k, v):
+        t[:, :3], t[:, 305:] = bad, bad
+    got = run_backward(q, k, v, d_out, opts)
+    for n, a, z in (("dq", 7, 161), ("dk", 3, 305), ("dv", 3, 305)):
+        compare({n: got[n][:, a:z]}, {n: ref[n][:, a:z], n + "_err": ref[n + "_err"][:, a:z]}, (n,))
+
+
+def test_backward_views_and_graph():
+    g = torch.Generator().manual_seed(14)
+    qkv = torch.randn(2, 150, 8 + 2 * 2, 64, generator=g).bfloat16().cuda()
+    views = qkv[:, :, :8], qkv[:, :, 8:10], qkv[:, :, 10:]
+    out, lse = ltxattn.masked_forward(*views, causal=True)
+    d_out = torch.randn(2, 150, 8, 64, generator=g).bfloat16().cuda()
+    ref = ltxattn.masked_backward(d_out, *(t.contiguous() for t in views), out, lse, causal=True)
+    # the gradients as parts of the projection's gradient
+    dqkv = torch.zeros_like(qkv)
+    into = dqkv[:, :, :8], dqkv[:, :, 8:10], dqkv[:, :, 10:]
+    ltxattn.masked_backward(d_out, *views, out, lse, *into, causal=True)
+    assert all(torch.equal(a, b) for a, b in zip(into, ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o2, l2 = ltxattn.masked_forward(*views, causal=True)
+        grads = ltxattn.masked_backward(d_out, *views, o2, l2, causal=True)
+    graph.replay()
+    torch.cuda.synchronize()
+    ltxattn.check()
+    assert all(torch.equal(a, b) for a, b in zip(grads, ref))
+
+
 @pytest.mark.parametrize("dim,q_len", [(64, 1), (64, 200), (128, 90), (128, 300)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 def test_what_is_masked_does_not_reach_a_result(dim, q_len, bad):
@@ -237,3 +367,12 @@ def test_refusals():
         with pytest.raises(ltxattn.LtxAttnError) as e:
             call()
         assert e.value.status == status
+    out, lse = ltxattn.masked_forward(q, k, v)
+    with pytest.raises(ValueError):
+        ltxattn.masked_backward(out, q, k, v, out, None)
+    with pytest.raises(ValueError):
+        ltxattn.masked_backward(out[:, :4], q, k, v, out, lse)
+    for bad in (dict(dq=q), dict(dk=torch.empty_like(k), dv=k), dict(dq=out)):
+        with pytest.raises(ltxattn.LtxAttnError) as e:
+            ltxattn.masked_backward(out.clone(), q, k, v, out, lse, **bad)
+        assert e.value.status == ltxattn.ERR_INVALID_ARG
