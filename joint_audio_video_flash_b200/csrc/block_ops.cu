@@ -121,7 +121,7 @@ int layer_norm_forward(ltx::NormParams& p, long long groups, cudaStream_t stream
 }
 
 // The plan of a backward call, the same for the workspace query and the launch.
-enum class GradKernel { kVector, kScalar8, kScalar16, kWide };
+enum class GradKernel { kVector2, kVector4, kScalar8, kScalar16, kWide };
 struct GradPlan {
   GradKernel kernel;
   int wpr, ctas_per_group;
@@ -141,8 +141,11 @@ int grad_plan(int cols, bool vector, bool affine, long long groups, long long ro
               GradPlan* plan) {
   constexpr int V = ltx::Elem<T>::kVec;
   int resident = 0;
-  if (vector && (plan->wpr = norm_warps(cols, 4 * V))) {
-    plan->kernel = GradKernel::kVector;
+  if (vector && (plan->wpr = norm_warps(cols, 2 * V))) {
+    plan->kernel = GradKernel::kVector2;
+    resident = grad_resident<T, V, 2>(affine);
+  } else if (vector && (plan->wpr = norm_warps(cols, 4 * V))) {
+    plan->kernel = GradKernel::kVector4;
     resident = grad_resident<T, V, 4>(affine);
   } else if (!vector && (plan->wpr = norm_warps(cols, 8))) {
     plan->kernel = GradKernel::kScalar8;
@@ -195,7 +198,8 @@ int layer_norm_grad(const ltx::NormParams& p, long long groups, bool affine,
   constexpr int V = ltx::Elem<T>::kVec;
   cudaError_t e = cudaSuccess;
   switch (plan.kernel) {
-    case GradKernel::kVector: e = launch_grad<T, V, 4>(p, groups, affine, stream); break;
+    case GradKernel::kVector2: e = launch_grad<T, V, 2>(p, groups, affine, stream); break;
+    case GradKernel::kVector4: e = launch_grad<T, V, 4>(p, groups, affine, stream); break;
     case GradKernel::kScalar8: e = launch_grad<T, 1, 8>(p, groups, affine, stream); break;
     case GradKernel::kScalar16: e = launch_grad<T, 1, 16>(p, groups, affine, stream); break;
     case GradKernel::kWide: {

@@ -116,8 +116,12 @@ struct NormWalk {
   }
 };
 
+// CTAs an SM must hold, by the elements a lane keeps of a row (the register cap).
+constexpr int norm_min_ctas(int elems) { return elems <= 16 ? 3 : elems <= 32 ? 2 : 1; }
+constexpr int norm_grad_min_ctas(int elems) { return elems <= 8 ? 3 : elems <= 16 ? 2 : 1; }
+
 template <typename T, int V, int kChunks>
-__global__ void __launch_bounds__(kNormThreads, 2)
+__global__ void __launch_bounds__(kNormThreads, norm_min_ctas(kChunks* V))
     ltx_layer_norm(const __grid_constant__ NormParams p) {
   using Chunk = NormChunk<T, V>;
   __shared__ float2 red[4][kNormWarps];
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 }
 
 template <typename T, int V, int kChunks, bool kAffine>
-__global__ void __launch_bounds__(kNormThreads, 2)
+__global__ void __launch_bounds__(kNormThreads, norm_grad_min_ctas(kChunks* V))
     ltx_layer_norm_grad(const __grid_constant__ NormParams p) {
   using Chunk = NormChunk<T, V>;
   __shared__ float2 red[2][kNormWarps];
@@ -227,6 +231,18 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   for (int c = 0; c < kSums; ++c)
 #pragma unroll
     for (int i = 0; i < V; ++i) dw[c][i] = db[c][i] = 0.0f;
+
+  // a CTA stays within one group: its columns' weights are loaded once
+  Chunk wc[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int e = (c * w.lanes + w.lane) * V;
+    if (weight && e < p.cols)
+      wc[c].load(weight + affine + e);
+    else
+      wc[c].zero();
+  }
+  const float unweighted = weight ? 0.0f : 1.0f;
 
   struct Row {
     Chunk x[kChunks], dy[kChunks];
@@ -255,21 +271,13 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     // row holds rstd = 0 and dy = 0
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int e = (c * w.lanes + w.lane) * V;
-      float xf[V], gf[V];
+      float xf[V], gf[V], wf[V];
       v.x[c].get(xf);
       v.dy[c].get(gf);
-      float wf[V];
-      if (weight && e < p.cols) {
-        Chunk wc;
-        wc.load(weight + affine + e);
-        wc.get(wf);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) wf[i] = 1.0f;
-      }
+      wc[c].get(wf);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
+        wf[i] += unweighted;
         const float z = (xf[i] - v.mean) * v.rstd;
         const float gz = gf[i] * z;
         if constexpr (kAffine) {
@@ -288,21 +296,14 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     for (int c = 0; c < kChunks; ++c) {
       const int e = (c * w.lanes + w.lane) * V;
       if (e >= p.cols) continue;
-      float xf[V], gf[V];
+      float xf[V], gf[V], wf[V];
       v.x[c].get(xf);
       v.dy[c].get(gf);
-      if (weight) {
-        Chunk wc;
-        float wf[V];
-        wc.load(weight + affine + e);
-        wc.get(wf);
-#pragma unroll
-        for (int i = 0; i < V; ++i) gf[i] *= wf[i];
-      }
+      wc[c].get(wf);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float z = (xf[i] - v.mean) * v.rstd;
-        xf[i] = v.rstd * (gf[i] - mg - z * mgz);
+        xf[i] = v.rstd * (gf[i] * (wf[i] + unweighted) - mg - z * mgz);
       }
       Chunk::put(dst + e, xf);
     }

@@ -8,6 +8,7 @@ call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -442,54 +443,41 @@ def combine(o_parts, lses, q_len: int, out=None, *, stream=None):
 BF16, FP16, FP32 = 0, 1, 2
 ROPE_LAYOUTS = {"pairs": 0, "halves": 1}
 
+# The calls below run at the size of one token too, where the host's time is the call's time:
+# a tensor is looked at once, and the current device and stream are asked for once a call.
+
+_Strides = ctypes.c_longlong * 3
+
+
+@functools.lru_cache(maxsize=1)
+def _dtype_codes() -> dict:
+    import torch
+    return {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
 
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
-    if t.dtype not in codes:
+    code = _dtype_codes().get(t.dtype)
+    if code is None:
         raise TypeError(f"dtype {t.dtype} is none of bfloat16, float16, float32")
-    return codes[t.dtype]
-
-
-def _check_cuda(name: str, t, dtype=None, shape=None, contiguous: bool = False) -> None:
-    """A CUDA tensor on the current device, of this dtype and shape where they are given."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be a {dtype or ''} CUDA tensor".replace("  ", " "))
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _check_heads(name: str, t, dtype, shape=None) -> None:
-    """A [batch, len, heads, head_dim] CUDA tensor with contiguous channels."""
-    _check_cuda(name, t, dtype, shape)
-    if t.dim() != 4 or 0 in t.shape:
-        raise ValueError(f"{name} must be a non-empty [batch, len, heads, head_dim] tensor")
-    if t.shape[3] > 1 and t.stride(3) != 1:
-        raise ValueError(f"the channels of {name} must be contiguous")
-
-
-def _strides(t):
-    return (ctypes.c_longlong * 3)(*t.stride()[:3])
+    return code
 
 
 class _OnStream:
-    """Allocations inside belong to `stream` (torch's allocator reuses their memory in that
+    """The current device (``device``) and the stream a call runs on (``handle``).  Allocations
+    inside the with-block belong to that stream (torch's allocator reuses their memory in that
     stream's order), and tensors given to ``used`` are not handed out again before the work
     queued on it is done."""
+    __slots__ = ("device", "handle", "stream", "scope")
 
     def __init__(self, stream):
         import torch
-        self.handle = _stream_handle(stream)
-        self.other = stream is not None and self.handle != int(
-            torch.cuda.current_stream().cuda_stream)
-        self.stream = stream
-        self.scope = torch.cuda.stream(stream) if self.other else None
+        self.device = torch.cuda.current_device()
+        self.handle = torch._C._cuda_getCurrentRawStream(self.device)
+        self.stream = self.scope = None
+        if stream is not None and int(stream.cuda_stream) != self.handle:
+            self.handle = int(stream.cuda_stream)
+            self.stream = stream
+            self.scope = torch.cuda.stream(stream)
 
     def __enter__(self):
         if self.scope is not None:
@@ -502,14 +490,51 @@ class _OnStream:
         return False
 
     def used(self, *tensors) -> None:
-        if self.other:
+        if self.stream is not None:
             for t in tensors:
                 if t is not None:
                     t.record_stream(self.stream)
 
 
-def _ptr(t) -> int | None:
-    return None if t is None else t.data_ptr()
+def _not_here(name: str, t, dtype, device: int):
+    """The error for a tensor that is not of this dtype on this CUDA device."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (dtype is not None and t.dtype != dtype):
+        return TypeError(f"{name} must be a {dtype or ''} CUDA tensor".replace("  ", " "))
+    return ValueError(f"{name} is on {t.device}, not on the current device cuda:{device}")
+
+
+def _check_cuda(name: str, t, device: int, dtype=None, shape=None) -> None:
+    """A contiguous CUDA tensor on `device`, of this dtype and shape where they are given."""
+    try:
+        here = t.get_device() == device and (dtype is None or t.dtype == dtype)
+    except AttributeError:
+        here = False
+    if not here:
+        raise _not_here(name, t, dtype, device)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _heads_strides(name: str, t, device: int, dtype, shape=None):
+    """Strides of a [batch, len, heads, head_dim] CUDA tensor with contiguous channels."""
+    try:
+        here = t.get_device() == device and (dtype is None or t.dtype == dtype)
+    except AttributeError:
+        here = False
+    if not here:
+        raise _not_here(name, t, dtype, device)
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
+    if len(size) != 4 or 0 in size:
+        raise ValueError(f"{name} must be a non-empty [batch, len, heads, head_dim] tensor")
+    sb, sl, sh, sd = t.stride()
+    if sd != 1 and size[3] > 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return _Strides(sb, sl, sh)
 
 
 def rope_frequencies(axis_dims, base: float = 10000.0) -> list[float]:
@@ -517,6 +542,17 @@ def rope_frequencies(axis_dims, base: float = 10000.0) -> list[float]:
     ``inv_freq`` of :func:`rope_axes` that turns each axis as a one-axis embedding of d
     channels turns."""
     return [float(base) ** (-2.0 * i / d) for d in axis_dims for i in range(d // 2)]
+
+
+@functools.lru_cache(maxsize=16)
+def _rope_axes_arrays(inv_freq: tuple, axis_dims: tuple):
+    """The C arrays of these numbers."""
+    dims = tuple(int(x) for x in axis_dims)
+    if not 1 <= len(dims) <= 4:
+        raise ValueError("axis_dims must name one to four axes")
+    if len(inv_freq) != sum(dims) // 2:
+        raise ValueError(f"{len(inv_freq)} frequencies for {sum(dims) // 2} rotated pairs")
+    return (ctypes.c_double * len(inv_freq))(*inv_freq), (ctypes.c_int * 4)(*dims)
 
 
 def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
@@ -530,85 +566,92 @@ def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
     the gradient.  The outputs may be the inputs (in place).
     """
     import torch
-    code = None
-    for name, t in (("q", q), ("k", k)):
-        if t is None and name == "k":
-            continue
-        _check_heads(name, t, None)
-        code = _dtype_code(t)
-    if k is not None and (k.dtype != q.dtype or k.shape[:2] != q.shape[:2]
-                          or k.shape[3] != q.shape[3]):
-        raise ValueError("k must have q's dtype, batch, length and head_dim")
-    axis_dims = [int(x) for x in axis_dims]
-    inv_freq = [float(x) for x in inv_freq]
-    if not 1 <= len(axis_dims) <= 4:
-        raise ValueError("axis_dims must name one to four axes")
-    if len(inv_freq) != sum(axis_dims) // 2:
-        raise ValueError(f"{len(inv_freq)} frequencies for {sum(axis_dims) // 2} rotated pairs")
-    if layout not in ROPE_LAYOUTS:
+    freq, dims = _rope_axes_arrays(tuple(inv_freq), tuple(axis_dims))
+    axes = len(axis_dims)
+    code_layout = ROPE_LAYOUTS.get(layout)
+    if code_layout is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    batch, length, heads, head_dim = q.shape
-    _check_cuda("positions", positions, torch.float32, contiguous=True)
-    if positions.dim() != 3 or tuple(positions.shape[1:]) != (length, len(axis_dims)) \
-            or positions.shape[0] not in (1, batch):
-        raise ValueError(f"positions must be [{batch} or 1, {length}, {len(axis_dims)}]")
     with _OnStream(stream) as on:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _check_heads("q_out", q_out, q.dtype, q.shape)
-        if k is None:
-            if k_out is not None:
-                raise ValueError("k_out without k")
-        else:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-            _check_heads("k_out", k_out, k.dtype, k.shape)
-        call = _RopeCall(
-            q=_ptr(q), k=_ptr(k), q_out=_ptr(q_out), k_out=_ptr(k_out), q_stride=_strides(q),
-            q_out_stride=_strides(q_out), positions=_ptr(positions),
-            inv_freq=(ctypes.c_double * len(inv_freq))(*inv_freq),
-            axis_dims=(ctypes.c_int * 4)(*axis_dims), axes=len(axis_dims),
-            positions_batch=positions.shape[0], batch=batch, len=length, heads=heads,
-            kv_heads=1 if k is None else k.shape[2], head_dim=head_dim, dtype=code,
-            layout=ROPE_LAYOUTS[layout], inverse=int(bool(inverse)))
+        device = on.device
+        q_strides = _heads_strides("q", q, device, None)
+        code = _dtype_code(q)
+        shape = q.shape
+        batch, length, heads, head_dim = shape
+        _check_cuda("positions", positions, device, torch.float32)
+        pos_batch = positions.shape[0] if positions.dim() == 3 else 0
+        if pos_batch not in (1, batch) or positions.shape[1:] != (length, axes):
+            raise ValueError(f"positions must be [{batch} or 1, {length}, {axes}]")
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        q_out_strides = _heads_strides("q_out", q_out, device, q.dtype, shape)
+        kv_heads, k_strides, k_out_strides = 1, _Strides(), _Strides()
         if k is not None:
-            call.k_stride, call.k_out_stride = _strides(k), _strides(k_out)
-        _check(load().ltxattn_rope_axes(ctypes.byref(call), ctypes.c_void_p(on.handle)),
-               "ltxattn_rope_axes")
+            k_strides = _heads_strides("k", k, device, None)
+            k_shape = k.shape
+            if k.dtype != q.dtype or k_shape[0] != batch or k_shape[1] != length \
+                    or k_shape[3] != head_dim:
+                raise ValueError("k must have q's dtype, batch, length and head_dim")
+            kv_heads = k_shape[2]
+            if k_out is None:
+                k_out = torch.empty(k_shape, dtype=k.dtype, device=k.device)
+            k_out_strides = _heads_strides("k_out", k_out, device, k.dtype, k_shape)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        call = _RopeCall(
+            q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+            None if k is None else k_out.data_ptr(), q_strides, k_strides, q_out_strides,
+            k_out_strides, positions.data_ptr(), freq, dims, axes, pos_batch, batch, length,
+            heads, kv_heads, head_dim, code, code_layout, bool(inverse))
+        _check(load().ltxattn_rope_axes(call, on.handle), "ltxattn_rope_axes")
         on.used(q, k, q_out, k_out, positions)
     return q_out, k_out
 
 
-def _norm_rows(name: str, t, dtype=None, shape=None):
+def _norm_rows(name: str, t, device: int, dtype=None, shape=None):
     """(rows, cols, row stride) of a [..., cols] CUDA tensor whose rows lie at one stride."""
-    _check_cuda(name, t, dtype, shape)
-    if t.dim() < 1 or t.numel() == 0:
+    try:
+        here = t.get_device() == device and (dtype is None or t.dtype == dtype)
+    except AttributeError:
+        here = False
+    if not here:
+        raise _not_here(name, t, dtype, device)
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
+    n = t.numel()
+    if len(size) < 1 or n == 0:
         raise ValueError(f"{name} must be a non-empty [..., cols] tensor")
-    cols = t.shape[-1]
-    if cols > 1 and t.stride(-1) != 1:
+    cols = size[-1]
+    if t.is_contiguous():
+        return n // cols, cols, cols
+    steps = t.stride()
+    if cols > 1 and steps[-1] != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
     stride, want = None, None
-    for size, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if size == 1:
+    for count, step in zip(reversed(size[:-1]), reversed(steps[:-1])):
+        if count == 1:
             continue
         if stride is None:
             stride = step
         elif step != want:
             raise ValueError(f"the rows of {name} must lie at one stride")
-        want = step * size
-    return t.numel() // cols, cols, cols if stride is None else stride
+        want = step * count
+    return n // cols, cols, cols if stride is None else stride
 
 
-def _norm_affine(weight, bias, x, rows: int, cols: int) -> int:
+def _norm_affine(weight, bias, x, rows: int, cols: int, device: int) -> int:
     """Groups of a weight (and bias) of shape [cols] or [groups, cols]."""
-    groups = 1
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        _check_cuda(name, t, x.dtype, contiguous=True)
-        if t.dim() not in (1, 2) or t.shape[-1] != cols:
-            raise ValueError(f"{name} must be [{cols}] or [groups, {cols}]")
-        if name == "bias" and (weight is None or t.shape != weight.shape):
-            raise ValueError("bias must have weight's shape")
-        groups = t.shape[0] if t.dim() == 2 else 1
+    if weight is None:
+        if bias is not None:
+            raise ValueError("a bias needs a weight")
+        return 1
+    _check_cuda("weight", weight, device, x.dtype)
+    shape = weight.shape
+    if len(shape) not in (1, 2) or shape[-1] != cols:
+        raise ValueError(f"weight must be [{cols}] or [groups, {cols}]")
+    if bias is not None:
+        _check_cuda("bias", bias, device, x.dtype, shape)
+    groups = shape[0] if len(shape) == 2 else 1
     if groups < 1 or rows % groups:
         raise ValueError(f"{rows} rows do not fall into {groups} equal groups")
     return groups
@@ -624,21 +667,21 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps: float = 1e-6,
     ``out`` may be x.
     """
     import torch
-    rows, cols, x_stride = _norm_rows("x", x)
-    code = _dtype_code(x)
-    groups = _norm_affine(weight, bias, x, rows, cols)
     with _OnStream(stream) as on:
+        rows, cols, x_stride = _norm_rows("x", x, on.device)
+        code = _dtype_code(x)
+        groups = _norm_affine(weight, bias, x, rows, cols, on.device)
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _, _, out_stride = _norm_rows("out", out, x.dtype, x.shape)
+            out_stride = cols
+        else:
+            out_stride = _norm_rows("out", out, on.device, x.dtype, x.shape)[2]
         mean = rstd = None
         if return_stats:
             mean, rstd = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
-        vp = ctypes.c_void_p
         _check(load().ltxattn_layer_norm(
-            vp(_ptr(x)), vp(_ptr(weight)), vp(_ptr(bias)), vp(_ptr(out)), vp(_ptr(mean)),
-            vp(_ptr(rstd)), rows, cols, groups, x_stride, out_stride, ctypes.c_float(eps), code,
-            vp(on.handle)), "ltxattn_layer_norm")
+            x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean), _ptr(rstd), rows,
+            cols, groups, x_stride, out_stride, eps, code, on.handle), "ltxattn_layer_norm")
         on.used(x, weight, bias, out)
     return (out, mean, rstd) if return_stats else out
 
@@ -651,17 +694,19 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, *, stream=None)
     or x.
     """
     import torch
-    rows, cols, x_stride = _norm_rows("x", x)
-    code = _dtype_code(x)
-    _, _, dy_stride = _norm_rows("dy", dy, x.dtype, x.shape)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _check_cuda(name, t, torch.float32, x.shape[:-1], contiguous=True)
-    groups = _norm_affine(weight, None, x, rows, cols)
     lib = load()
     with _OnStream(stream) as on:
+        device = on.device
+        rows, cols, x_stride = _norm_rows("x", x, device)
+        code = _dtype_code(x)
+        dy_stride = _norm_rows("dy", dy, device, x.dtype, x.shape)[2]
+        stats = x.shape[:-1]
+        _check_cuda("mean", mean, device, torch.float32, stats)
+        _check_cuda("rstd", rstd, device, torch.float32, stats)
+        groups = _norm_affine(weight, None, x, rows, cols, device)
         if dx is None:
             dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        _, _, dx_stride = _norm_rows("dx", dx, x.dtype, x.shape)
+        dx_stride = _norm_rows("dx", dx, device, x.dtype, x.shape)[2]
         dweight = dbias = workspace = None
         need = ctypes.c_ulonglong(0)
         if weight is not None:
@@ -671,61 +716,58 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, *, stream=None)
                    "ltxattn_layer_norm_workspace")
             if need.value:
                 workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        vp = ctypes.c_void_p
         _check(lib.ltxattn_layer_norm_backward(
-            vp(_ptr(dy)), vp(_ptr(x)), vp(_ptr(weight)), vp(_ptr(mean)), vp(_ptr(rstd)),
-            vp(_ptr(dx)), vp(_ptr(dweight)), vp(_ptr(dbias)), rows, cols, groups, dy_stride,
-            x_stride, dx_stride, code, vp(_ptr(workspace)), need.value, vp(on.handle)),
+            dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
+            dx.data_ptr(), _ptr(dweight), _ptr(dbias), rows, cols, groups, dy_stride, x_stride,
+            dx_stride, code, _ptr(workspace), need.value, on.handle),
             "ltxattn_layer_norm_backward")
         on.used(dy, x, mean, rstd, weight, dx)
     return dx, dweight, dbias
 
 
-def _masked_call(q, k, v, out, lse, scale, softcap, slopes, causal, prefix, q_starts, kv_starts):
-    """Checks what the library cannot see from raw pointers; returns the filled _MaskedCall."""
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_starts, kv_starts):
+    """Checks what the library cannot see from raw pointers; returns the _MaskedCall, out and
+    lse not filled in."""
     import torch
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_heads(name, t, torch.bfloat16)
+    bf16 = torch.bfloat16
+    q_strides = _heads_strides("q", q, device, bf16)
+    k_strides = _heads_strides("k", k, device, bf16)
     batch, q_len, heads, head_dim = q.shape
-    kv_len, kv_heads = k.shape[1:3]
-    if k.shape[0] != batch or k.shape[3] != head_dim or v.shape != k.shape:
+    k_shape = k.shape
+    if k_shape[0] != batch or k_shape[3] != head_dim or v.shape != k_shape:
         raise ValueError("k and v must be [batch, kv_len, kv_heads, head_dim] matching q")
-    if (q_starts is None) != (kv_starts is None):
-        raise ValueError("q_starts and kv_starts come together")
+    v_strides = _heads_strides("v", v, device, bf16)
     docs = 0
-    if q_starts is not None:
+    if q_starts is not None or kv_starts is not None:
+        if q_starts is None or kv_starts is None:
+            raise ValueError("q_starts and kv_starts come together")
         if q_starts.dim() != 2 or q_starts.shape[1] < 2:
             raise ValueError("q_starts must be [batch, documents + 1]")
         docs = q_starts.shape[1] - 1
-        for name, t in (("q_starts", q_starts), ("kv_starts", kv_starts)):
-            _check_cuda(name, t, torch.int32, (batch, docs + 1), contiguous=True)
+        _check_cuda("q_starts", q_starts, device, torch.int32, (batch, docs + 1))
+        _check_cuda("kv_starts", kv_starts, device, torch.int32, (batch, docs + 1))
     if prefix is not None:
         if not causal:
             raise ValueError("a prefix needs causal=True (without it every key is visible)")
-        _check_cuda("prefix", prefix, torch.int32, (batch, max(docs, 1)), contiguous=True)
+        _check_cuda("prefix", prefix, device, torch.int32, (batch, max(docs, 1)))
     if slopes is not None:
-        _check_cuda("slopes", slopes, torch.float32, (heads,), contiguous=True)
-    if out is not None:
-        _check_heads("out", out, torch.bfloat16, q.shape)
-    if lse is not None:
-        _check_cuda("lse", lse, torch.float32, (batch, heads, q_len), contiguous=True)
-    call = _MaskedCall(
-        q=_ptr(q), k=_ptr(k), v=_ptr(v), out=_ptr(out), lse=_ptr(lse), q_stride=_strides(q),
-        k_stride=_strides(k), v_stride=_strides(v), batch=batch, q_len=q_len, kv_len=kv_len,
-        heads=heads, kv_heads=kv_heads, head_dim=head_dim,
-        scale=1.0 / math.sqrt(head_dim) if scale is None else float(scale),
-        softcap=float(softcap), slopes=_ptr(slopes), prefix=_ptr(prefix),
-        q_starts=_ptr(q_starts), kv_starts=_ptr(kv_starts), docs=docs, causal=int(bool(causal)))
-    if out is not None:
-        call.out_stride = _strides(out)
-    return call
+        _check_cuda("slopes", slopes, device, torch.float32, (heads,))
+    return _MaskedCall(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, q_strides, k_strides, v_strides,
+        _Strides(), batch, q_len, k_shape[1], heads, k_shape[2], head_dim,
+        1.0 / math.sqrt(head_dim) if scale is None else scale, softcap, _ptr(slopes),
+        _ptr(prefix), _ptr(q_starts), _ptr(kv_starts), docs, bool(causal))
 
 
 def _masked_workspace(call, backward: bool, device):
     import torch
     need = ctypes.c_ulonglong(0)
-    _check(load().ltxattn_masked_workspace(ctypes.byref(call), int(backward),
-                                           ctypes.byref(need)), "ltxattn_masked_workspace")
+    _check(load().ltxattn_masked_workspace(call, backward, ctypes.byref(need)),
+           "ltxattn_masked_workspace")
     return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
 
 
@@ -744,22 +786,24 @@ def masked_forward(q, k, v, out=None, lse=None, *, scale: float | None = None,
     when they are allocated here).
     """
     import torch
-    call = _masked_call(q, k, v, out, lse, scale, softcap, slopes, causal, prefix, q_starts,
-                        kv_starts)
     with _OnStream(stream) as on:
+        device = on.device
+        call = _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_starts,
+                            kv_starts)
         if out is None:  # rows of no document stay as they are made here
             make = torch.empty if q_starts is None else torch.zeros
             out = make(q.shape, dtype=q.dtype, device=q.device)
-            call.out, call.out_stride = _ptr(out), _strides(out)
+        call.out_stride = _heads_strides("out", out, device, torch.bfloat16, q.shape)
+        shape = (call.batch, call.heads, call.q_len)
         if lse is None:
-            shape = (q.shape[0], q.shape[2], q.shape[1])
             lse = torch.empty(shape, dtype=torch.float32, device=q.device) if q_starts is None \
                 else torch.full(shape, -math.inf, dtype=torch.float32, device=q.device)
-            call.lse = _ptr(lse)
+        else:
+            _check_cuda("lse", lse, device, torch.float32, shape)
+        call.out, call.lse = out.data_ptr(), lse.data_ptr()
         workspace = _masked_workspace(call, False, q.device)
         _check(load().ltxattn_masked_forward(
-            ctypes.byref(call), ctypes.c_void_p(_ptr(workspace)),
-            0 if workspace is None else workspace.numel(), ctypes.c_void_p(on.handle)),
+            call, _ptr(workspace), 0 if workspace is None else workspace.numel(), on.handle),
             "ltxattn_masked_forward")
         on.used(q, k, v, out, lse, slopes, prefix, q_starts, kv_starts)
     return out, lse
@@ -775,26 +819,29 @@ def masked_backward(d_out, q, k, v, out, lse, dq=None, dk=None, dv=None, *,
     of no document keep what dq, dk and dv held (zeros when they are allocated here).
     """
     import torch
-    call = _masked_call(q, k, v, out, lse, scale, softcap, slopes, causal, prefix, q_starts,
-                        kv_starts)
     if out is None or lse is None:
         raise ValueError("out and lse of the forward call are needed")
-    _check_heads("d_out", d_out, torch.bfloat16, q.shape)
     with _OnStream(stream) as on:
+        device, bf16 = on.device, torch.bfloat16
+        call = _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_starts,
+                            kv_starts)
+        call.out_stride = _heads_strides("out", out, device, bf16, q.shape)
+        _check_cuda("lse", lse, device, torch.float32, (call.batch, call.heads, call.q_len))
+        call.out, call.lse = out.data_ptr(), lse.data_ptr()
+        d_out_strides = _heads_strides("d_out", d_out, device, bf16, q.shape)
         make = torch.empty if q_starts is None else torch.zeros
-        grads = []
+        grads, strides = [], []
         for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             if t is None:
-                t = make(like.shape, dtype=like.dtype, device=like.device)
-            _check_heads(name, t, torch.bfloat16, like.shape)
+                t = make(like.shape, dtype=bf16, device=like.device)
+            strides.append(_heads_strides(name, t, device, bf16, like.shape))
             grads.append(t)
         dq, dk, dv = grads
-        grad = _MaskedGrad(d_out=_ptr(d_out), dq=_ptr(dq), dk=_ptr(dk), dv=_ptr(dv),
-                           d_out_stride=_strides(d_out), dq_stride=_strides(dq),
-                           dk_stride=_strides(dk), dv_stride=_strides(dv))
+        grad = _MaskedGrad(d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                           d_out_strides, *strides)
         workspace = _masked_workspace(call, True, q.device)
-        _check(load().ltxattn_masked_backward(
-            ctypes.byref(call), ctypes.byref(grad), ctypes.c_void_p(_ptr(workspace)),
-            workspace.numel(), ctypes.c_void_p(on.handle)), "ltxattn_masked_backward")
+        _check(load().ltxattn_masked_backward(call, grad, workspace.data_ptr(),
+                                              workspace.numel(), on.handle),
+               "ltxattn_masked_backward")
         on.used(d_out, q, k, v, out, lse, dq, dk, dv, slopes, prefix, q_starts, kv_starts)
     return dq, dk, dv
