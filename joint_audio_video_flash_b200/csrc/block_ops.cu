@@ -53,15 +53,27 @@ bool views_apart(const View& a, const View& b) {
   return off >= wa && off + wb <= bytes;
 }
 
-template <typename T>
-cudaError_t launch_rope(const ltx::RopeParams& p, bool halves, cudaStream_t stream) {
+template <typename T, bool kHalves>
+int launch_rope(ltx::RopeParams& p, cudaStream_t stream) {
+  const int resident = ltx::resident_ctas<ltx::ltx_rope_axes<T, kHalves>>(ltx::kRopeThreads);
+  if (resident < 1) return LTXATTN_ERR_CUDA;
+  constexpr int kChunk = ltx::Elem<T>::kVec, kHeads = ltx::kRopeHeads / (kHalves ? 2 : 1);
+  p.units = p.head_dim / (kHalves ? 2 * kChunk : kChunk);
+  const int slots = ltx::kRopeThreads / p.units;  // units <= 128
+  // as few threads to a token as still hold its heads, so that every thread has its full step
+  p.head_slots = std::min((p.heads + kHeads - 1) / kHeads, slots);
+  p.tokens = slots / p.head_slots;
+  p.steps = (p.heads + p.head_slots * kHeads - 1) / (p.head_slots * kHeads);
   const long long rows = (long long)p.batch * p.len;
-  const unsigned grid = (unsigned)((rows + p.tokens - 1) / p.tokens);
-  if (halves)
-    ltx::ltx_rope_axes<T, true><<<grid, ltx::kRopeThreads, 0, stream>>>(p);
-  else
-    ltx::ltx_rope_axes<T, false><<<grid, ltx::kRopeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const unsigned grid =
+      (unsigned)std::min<long long>((rows + p.tokens - 1) / p.tokens, resident);
+  ltx::ltx_rope_axes<T, kHalves><<<grid, ltx::kRopeThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+}
+
+template <typename T>
+int launch_rope(ltx::RopeParams& p, bool halves, cudaStream_t stream) {
+  return halves ? launch_rope<T, true>(p, stream) : launch_rope<T, false>(p, stream);
 }
 
 // ---------------------------------------------------------------- layer norm
@@ -348,16 +360,12 @@ int ltxattn_rope_axes(const ltxattn_rope_call* call, ltxattn_stream_t stream_) {
     p.freq[i].x = (float)turns;
     p.freq[i].y = (float)(turns - (double)p.freq[i].x);
   }
-  const int chunk = 16 / item;
-  p.units = a.head_dim / (halves ? 2 * chunk : chunk);
-  const int slots = ltx::kRopeThreads / p.units;  // units <= 128
-  p.head_slots = std::min(p.heads, slots);
-  p.tokens = slots / p.head_slots;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const cudaError_t e = a.dtype == LTXATTN_BF16   ? launch_rope<__nv_bfloat16>(p, halves, stream)
-                        : a.dtype == LTXATTN_FP16 ? launch_rope<__half>(p, halves, stream)
-                                                  : launch_rope<float>(p, halves, stream);
-  return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+  switch (a.dtype) {
+    case LTXATTN_BF16: return launch_rope<__nv_bfloat16>(p, halves, stream);
+    case LTXATTN_FP16: return launch_rope<__half>(p, halves, stream);
+    default: return launch_rope<float>(p, halves, stream);
+  }
 }
 
 int ltxattn_layer_norm(const void* x, const void* weight, const void* bias, void* out,
