@@ -81,21 +81,10 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The score of a raw product in log2 units, and d score / d raw product over scale (kCap).
-template <bool kCap, bool kBias>
-__device__ __forceinline__ float masked_score(float raw, const MaskedShape& p, float slope_log2,
-                                              float far, float& bend) {
-  float s;
-  if constexpr (kCap) {
-    const float t = tanh_ex2(raw * p.cap_in);
-    s = t * p.cap_log2;
-    bend = fmaf(-t, t, 1.0f);
-  } else {
-    s = raw * p.scale_log2;
-    bend = 1.0f;
-  }
-  if constexpr (kBias) s = fmaf(-slope_log2, fabsf(far), s);
-  return s;
+// 1 - tanh^2 of a capped score (log2 units).
+__device__ __forceinline__ float cap_bend(float capped, float inv_cap_log2) {
+  const float t = capped * inv_cap_log2;
+  return fmaf(-t, t, 1.0f);
 }
 
 // Sets the rows [live, 128) of a staged tile to zero (whole warp, generic proxy, then a fence
@@ -446,6 +435,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       qt += begin % per_head;
     }
     float slope = 0.0f;
+    const float inv_cap = kCap ? 1.0f / p.s.cap_log2 : 0.0f;
     // lse and delta of the columns, one step ahead: a lane holds columns lane and lane + 32
     float2 next[2];
     auto fetch = [&](int hh, int tile) {
@@ -483,7 +473,15 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         tmem_ld32(trow + L::kColS + g * 64 + c * 32, *reinterpret_cast<float(*)[32]>(&s[c * 32]));
       tmem_ld_wait();
       const bool masked = from_warp > i0;
-      const float place = (float)(i0 + (m.nk - m.nq) - j);
+      float bent[kCap ? 64 : 1];
+      if constexpr (kCap) {
+        masked_scores<true, false>(s, p.s, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int x = 0; x < 64; ++x) bent[x] = cap_bend(s[x], inv_cap);
+        if constexpr (kBias) masked_bias<true>(s, p.s, slope, (float)(i0 + (m.nk - m.nq) - j), 1.0f);
+      } else if constexpr (kBias) {
+        masked_bias<false>(s, p.s, slope, (float)(i0 + (m.nk - m.nq) - j), 1.0f);
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];
@@ -495,14 +493,10 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int q = c * 32 + x + y;
-            float bend, a;
-            if constexpr (kCap || kBias)
-              a = masked_score<kCap, kBias>(s[q], p.s, slope, place + (float)q, bend) - l[y];
-            else
-              a = fmaf(s[q], p.s.scale_log2, -l[y]);
+            float a = kCap || kBias ? s[q] - l[y] : fmaf(s[q], p.s.scale_log2, -l[y]);
             if (masked && i0 + q < from) a = -INFINITY;
             e[y] = ex2(a);
-            s[q] = kCap ? e[y] * bend : e[y];
+            s[q] = kCap ? e[y] * bent[q] : e[y];
           }
           pk[x / 2] = pack_bf16x2(e[0], e[1]);
           pk[x / 2 + 1] = pack_bf16x2(e[2], e[3]);
@@ -815,6 +809,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     const int lim_warp = masked_limit(m, p.s.causal, i0 + wq * 32);
     float slope = 0.0f;
     if constexpr (kBias) slope = __ldg(p.s.slopes + h) * 1.4426950408889634f;
+    const float inv_cap = kCap ? 1.0f / p.s.cap_log2 : 0.0f;
     const int place = i + m.nk - m.nq;
     bool ok = !*abort_flag;
     for (int t = 0; t < n && ok; ++t) {
@@ -829,16 +824,20 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       tmem_ld_wait();
       const int kv0 = (begin + t) * kBlockN + g * 64;
       const bool masked = kv0 + 64 > lim_warp;
-      const float far0 = (float)(place - kv0);
+      float bent[kCap ? 64 : 1];
+      if constexpr (kCap) {
+        masked_scores<true, false>(s, p.s, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int x = 0; x < 64; ++x) bent[x] = cap_bend(s[x], inv_cap);
+        if constexpr (kBias) masked_bias<true>(s, p.s, slope, (float)(place - kv0), -1.0f);
+      } else if constexpr (kBias) {
+        masked_bias<false>(s, p.s, slope, (float)(place - kv0), -1.0f);
+      }
 #pragma unroll
       for (int c = 0; c < 64; ++c) {
-        float bend, a;
-        if constexpr (kCap || kBias)
-          a = masked_score<kCap, kBias>(s[c], p.s, slope, far0 - (float)c, bend) - st.x;
-        else
-          a = fmaf(s[c], p.s.scale_log2, -st.x);
+        float a = kCap || kBias ? s[c] - st.x : fmaf(s[c], p.s.scale_log2, -st.x);
         if (masked && kv0 + c >= lim) a = -INFINITY;
-        s[c] = kCap ? ex2(a) * bend : ex2(a);
+        s[c] = kCap ? ex2(a) * bent[c] : ex2(a);
       }
       ok = __all_sync(0xffffffffu, mbar_wait(bar(L::bDp), (uint32_t)t & 1u, ctl));
       if (!ok) break;

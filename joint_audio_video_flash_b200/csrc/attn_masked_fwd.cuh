@@ -61,6 +61,8 @@ struct MaskedShape {
   float scale_log2;            // scale * log2(e)
   float cap_in;                // scale / cap
   float cap_log2;              // cap * log2(e)
+  float cap_poly[6];           // cap_log2 tanh(cap_in s) = s P(s^2) for |s| <= cap_limit
+  float cap_limit;
   const float* slopes;         // [heads] (kBias)
   int* status;
   unsigned long long timeout_ns;
@@ -187,18 +189,78 @@ struct MaskedSmem {
   static constexpr uint32_t kTmemCols = 512;
 };
 
-// Turns 128 raw scores into scores in log2 units when they are capped or biased.
-template <bool kCap, bool kBias>
-__device__ __forceinline__ void masked_scores(float* s, const MaskedShape& p, float slope_log2,
-                                              float place) {
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Subtracts slope_log2 |far0 + dir c| from a thread's N scores, after the scale when they are
+// still raw (kScaled = false).  Whole warp.  Where no element of the warp lies on the
+// diagonal's other side, |distance| is linear in the column and takes one packed multiply-add.
+template <bool kScaled, int N>
+__device__ __forceinline__ void masked_bias(float (&s)[N], const MaskedShape& p,
+                                            float slope_log2, float far0, float dir) {
+  const float far1 = far0 + dir * (float)(N - 1);
+  const bool ahead = __all_sync(0xffffffffu, fminf(far0, far1) >= 0.0f);
+  const bool behind = __all_sync(0xffffffffu, fmaxf(far0, far1) <= 0.0f);
+  if (ahead || behind) {
+    const float k = ahead ? -slope_log2 : slope_log2;
+    const float2 step = make_float2(k * dir, k * dir), base = make_float2(k * far0, k * far0);
+    const float2 scale = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
-  for (int c = 0; c < kBlockN; ++c) {
-    if constexpr (kCap)
-      s[c] = tanh_ex2(s[c] * p.cap_in) * p.cap_log2;
-    else
-      s[c] *= p.scale_log2;
-    if constexpr (kBias) s[c] = fmaf(-slope_log2, fabsf(place - (float)c), s[c]);
+    for (int c = 0; c < N; c += 2) {
+      const float2 b = __ffma2_rn(make_float2((float)c, (float)(c + 1)), step, base);
+      const float2 x = make_float2(s[c], s[c + 1]);
+      const float2 r = kScaled ? __fadd2_rn(x, b) : __ffma2_rn(x, scale, b);
+      s[c] = r.x;
+      s[c + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      s[c] = fmaf(-slope_log2, fabsf(fmaf(dir, (float)c, far0)),
+                  kScaled ? s[c] : s[c] * p.scale_log2);
   }
+}
+
+// Turns a thread's N raw products into scores in log2 units when they are capped or biased;
+// far0 + dir * c is the distance of element c.  Whole warp.
+//
+// The cap: tanh through the MUFU costs two of its operations per element ahead of the
+// softmax's own, three times what the products take.  While every product of the warp lies
+// within the cap (|scale q.k| <= cap: the usual case, as a cap is there for the outliers),
+// cap tanh(s / cap) is an odd polynomial of degree 11 in packed fused multiply-adds, with a
+// largest error of 3.2e-7 cap in fp32 (the coefficients are a least-squares fit of tanh on
+// [-1, 1], reweighted until its ripples are level).
+// Measured at 8192 x 8192 x 16 heads x 128: TBD us against 1229 us with tanh_ex2 alone.
+template <bool kCap, bool kBias, int N>
+__device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& p,
+                                              float slope_log2, float far0, float dir) {
+  if constexpr (kCap) {
+    float lo = fmin3(s[0], s[1], s[2]);
+#pragma unroll
+    for (int c = 3; c + 1 < N; c += 2) lo = fmin3(lo, s[c], s[c + 1]);
+    lo = fminf(lo, s[N - 1]);
+    if (__any_sync(0xffffffffu, fmaxf(row_max<N>(s), -lo) > p.cap_limit)) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) s[c] = tanh_ex2(s[c] * p.cap_in) * p.cap_log2;
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const float2 x = make_float2(s[c], s[c + 1]);
+        const float2 y = __fmul2_rn(x, x);
+        float2 r = make_float2(p.cap_poly[5], p.cap_poly[5]);
+#pragma unroll
+        for (int k = 4; k >= 0; --k)
+          r = __ffma2_rn(r, y, make_float2(p.cap_poly[k], p.cap_poly[k]));
+        r = __fmul2_rn(r, x);
+        s[c] = r.x;
+        s[c + 1] = r.y;
+      }
+    }
+  }
+  if constexpr (kBias) masked_bias<kCap>(s, p, slope_log2, far0, dir);
 }
 
 template <int D, bool kAlt, bool kCap, bool kBias>
@@ -459,7 +521,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         tmem_ld_wait();
         const int kv0 = (begin + (kAlt ? 2 * step + g : step)) * kBlockN;
         if constexpr (kTransform)
-          masked_scores<kCap, kBias>(s, p.s, slope, (float)(place - kv0));
+          masked_scores<kCap, kBias>(s, p.s, slope, (float)(place - kv0), -1.0f);
         if (kv0 + kBlockN > lim_warp) {
           const int to = lim - kv0;
 #pragma unroll

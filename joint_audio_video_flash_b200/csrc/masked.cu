@@ -162,6 +162,17 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
   if (a.softcap > 0.0f) {
     s.cap_in = a.scale / a.softcap;
     s.cap_log2 = a.softcap * kLog2e;
+    // tanh(x) = x P(x^2) on [-1, 1], rescaled to take raw products; where a coefficient would
+    // leave the normal fp32 range the limit of 0 leaves every product to the general form
+    const double tanh_poly[6] = {0.9999968409538269,   -0.3332400321960449,
+                                 0.13253524899482727,  -0.05097284913063049,
+                                 0.016114167869091034, -0.0028394602704793215};
+    s.cap_limit = 1.0f / s.cap_in;
+    for (int i = 0; i < 6; ++i) {
+      const double c = tanh_poly[i] * (double)s.cap_log2 * std::pow((double)s.cap_in, 2 * i + 1);
+      s.cap_poly[i] = (float)c;
+      if (!(std::fabs(c) > 1e-37 && std::fabs(c) < 1e37)) s.cap_limit = 0.0f;
+    }
   }
   s.slopes = a.slopes;
   s.status = c.d_status;
