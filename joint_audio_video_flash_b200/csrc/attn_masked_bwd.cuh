@@ -7,6 +7,17 @@
 // with t = tanh(scale q.k / cap) (kCap; 1 - t^2 is absent without a cap) and P, dS zero where
 // the mask hides a key.
 //
+// delta comes from the forward call's bf16 out, whose rounding the differences dP - delta feel
+// where the softmax is peaked.  ltx_masked_bwd_q, which runs first, sums
+// e_i = sum_j P_ij (dP_ij - delta_i) in fp32 on its way: delta_i + e_i is free of out's rounding,
+// and that is what ltx_masked_bwd_kv gets.  dQ's own share of the error is -e_i sum_j P_ij b_ij
+// K_j (b the cap's derivative).  With a cap (kCap), which is there because scores are large, the
+// kernel carries that sum as a second accumulator and takes it out: the softmax's arithmetic
+// bounds it there, so the product is nearly free.  Without a cap it would add a third to the
+// bound of the kernel for errors that scores of ordinary size do not show (measured against 64
+// bits, relative to the gradient's norm: dQ 2.4e-3 without it at N(0, 1) scores, of which 1.7e-3
+// is the rounding of the result; capped scores of deviation 4: 3.6e-3 without, TBD with it).
+//
 // Two kernels instead of one: ltx_masked_bwd_kv owns a tile of 128 keys and walks the queries
 // that see it (dK and dV stay in TMEM, the query heads that share the key head one after the
 // other), ltx_masked_bwd_q owns 128 queries and walks their keys (dQ stays in TMEM).  S and dP
@@ -36,14 +47,15 @@ namespace ltx {
 
 struct MaskedBwdParams {
   MaskedShape s;
-  const float2* stat;  // [batch][heads][q_len]: lse (+inf for a query that sees no key), delta
+  float2* stat;        // [batch][heads][q_len]: lse (+inf for a query that sees no key), delta
   float scale;
   int parts;           // parts of the walk, each with an fp32 partial
   __nv_bfloat16* d0;   // dQ, or dK
   __nv_bfloat16* d1;   // dV
   long long stride0[3], stride1[3];  // batch, token, head
-  float* part0;        // [parts][batch][heads | kv_heads][len][D]
-  float* part1;
+  float* part0;        // [parts][batch][heads | kv_heads][len][D]: dQ or dK
+  float* part1;        // dV; sum P b K (dQ with a cap)
+  float* part_e;       // [parts][batch][heads][len]: e (dQ)
 };
 
 constexpr int kStatTokens = 64;  // tokens per CTA of ltx_masked_stat
@@ -103,10 +115,12 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int live) {
 // Writes 128 rows of D fp32 accumulator columns, times `scale`: bf16 rows through the staging
 // tile (each warp its own rows, whole rows by neighbouring lanes), or an fp32 partial.  One
 // warpgroup; row r of the tile is row first + r of the document, live rows come before n.
+// tfix: columns of a second accumulator, of which `fix` times is taken off (0: none).
 template <int D>
 __device__ __forceinline__ void masked_store(uint32_t tcol, bool some, float scale, uint8_t* stage,
                                              int first, int n, __nv_bfloat16* out,
-                                             long long row_stride, float* part) {
+                                             long long row_stride, float* part,
+                                             uint32_t tfix = 0u, float fix = 0.0f) {
   constexpr int kBoxBytes = kBlockM * 128;
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3;
   const int row = wq * 32 + lane;
@@ -117,6 +131,13 @@ __device__ __forceinline__ void masked_store(uint32_t tcol, bool some, float sca
       __syncwarp();
       tmem_ld32(tcol + c * 32, o);
       tmem_ld_wait();
+      if (tfix) {
+        float f[32];
+        tmem_ld32(tfix + c * 32, f);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = fmaf(-fix, f[x], o[x]);
+      }
     }
 #pragma unroll
     for (int x = 0; x < 32; ++x) o[x] = some ? o[x] * scale : 0.0f;
@@ -211,12 +232,11 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int hk = blockIdx.y;
-  const int b = (int)blockIdx.z / p.parts;
-  const int part = (int)blockIdx.z % p.parts;
+  const MaskedPlace at_work = masked_place(p.s.kv_heads, p.s.batch, p.parts);
+  const int hk = at_work.head, b = at_work.b, part = at_work.part;
 
   if (warp == 2) {
-    const MaskedDoc m = masked_find<true>(p.s, b, (int)blockIdx.x, kBlockN);
+    const MaskedDoc m = masked_find<true>(p.s, b, at_work.unit, kBlockN);
     if (lane == 0) *shared_doc = m;
   }
   if (threadIdx.x == 0) {
@@ -444,7 +464,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         const int i = tile * kBlockM + g * 64 + x * 32 + lane;
         next[x] = make_float2(INFINITY, 0.0f);  // no query there: P = 0
         if (i < m.nq)
-          next[x] = __ldg(p.stat + ((size_t)b * p.s.heads + hh) * p.s.q_len + m.q0 + i);
+          next[x] = p.stat[((size_t)b * p.s.heads + hh) * p.s.q_len + m.q0 + i];
       }
     };
     bool ok = !*abort_flag;
@@ -562,8 +582,11 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 // ---------------------------------------------------------------------------------------------
 // dQ of 128 queries of one head
 // ---------------------------------------------------------------------------------------------
-template <int D>
+// kFix: the second accumulator, sum P b K, takes the columns of the second S buffer; P b is then
+// written over S, which is free again when its product has read it.
+template <int D, bool kFix>
 struct BwdQSmem {
+  static constexpr int kSBuf = kFix ? 1 : 2;
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kBlockM * 128;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
@@ -574,7 +597,8 @@ struct BwdQSmem {
   static constexpr int kDo = kQ + kTileBytes;
   static constexpr int kK = kDo + kTileBytes;
   static constexpr int kV = kK + kKStages * kTileBytes;
-  static constexpr int kBar = kV + kVStages * kTileBytes;
+  static constexpr int kSum = kV + kVStages * kTileBytes;  // [128] fp32: e of group 1
+  static constexpr int kBar = kSum + 128 * 4;
   static constexpr int bQF = 0;
   static constexpr int bOF = 1;
   static constexpr int bKF = 2;
@@ -583,7 +607,8 @@ struct BwdQSmem {
   static constexpr int bVE = bVF + kVStages;
   static constexpr int bS = bVE + kVStages;  // 2: S computed, per buffer
   static constexpr int bDp = bS + 2;
-  static constexpr int bDs = bDp + 1;        // 2: dS written, per softmax warpgroup
+  static constexpr int bP = bDp + 1;         // 2: P b written (kFix), per softmax warpgroup
+  static constexpr int bDs = bP + 2;         // 2: dS written
   static constexpr int bEnd = bDs + 2;
   static constexpr int bDrain = bEnd + 1;
   static constexpr int kNumBars = bDrain + 1;
@@ -594,7 +619,8 @@ struct BwdQSmem {
   static constexpr int kRaw = ((kUsed + 1024 + 1023) / 1024) * 1024;
   static constexpr int kAlloc = kRaw > kMinSmemFor1Cta ? kRaw : kMinSmemFor1Cta;
   static_assert(kAlloc <= 227 * 1024, "shared memory of one SM");
-  static constexpr uint32_t kColS = 0;  // two buffers
+  static constexpr uint32_t kColS = 0;  // kSBuf buffers
+  static constexpr uint32_t kColPk = 128;  // kFix
   static constexpr uint32_t kColDp = 256, kColQ = 384;
   static constexpr uint32_t kTmemCols = 512;
 };
@@ -606,7 +632,9 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
                      const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ MaskedBwdParams p) {
-  using L = BwdQSmem<D>;
+  constexpr bool kFix = kCap;
+  using L = BwdQSmem<D, kFix>;
+  constexpr int kSBuf = L::kSBuf;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -618,14 +646,12 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
+  const MaskedPlace at_work = masked_place(p.s.heads, p.s.batch, p.parts);
+  const int h = at_work.head, b = at_work.b, part = at_work.part;
   const int hk = h / p.s.group;
-  const int b = (int)blockIdx.z / p.parts;
-  const int part = (int)blockIdx.z % p.parts;
 
   if (warp == 2) {
-    const int unit = p.s.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-    const MaskedDoc m = masked_find<false>(p.s, b, unit, kBlockM);
+    const MaskedDoc m = masked_find<false>(p.s, b, at_work.unit, kBlockM);
     if (lane == 0) *shared_doc = m;
   }
   if (threadIdx.x == 0) {
@@ -641,6 +667,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(bar(L::bS + g), 1);
+      mbar_init(bar(L::bP + g), 4);
       mbar_init(bar(L::bDs + g), 4);
     }
     mbar_init(bar(L::bDp), 1);
@@ -755,7 +782,8 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         if (!wt(bar(L::bKF + st), (uint32_t)(t / L::kKStages) & 1u)) return false;
         const int live = last_key - (begin + t) * kBlockN;
         if (live < kBlockN) zero_rows<L::kBoxes>(smem + L::kK + st * L::kTileBytes, live);
-        scores(L::kColS + 128 * (t & 1), dq, dk, (uint32_t)st * L::kTileBytes, L::bS + (t & 1));
+        scores(L::kColS + 128 * (t % kSBuf), dq, dk, (uint32_t)st * L::kTileBytes,
+               L::bS + t % kSBuf);
         return true;
       };
       auto dp_of = [&](int t) -> bool {
@@ -767,26 +795,35 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         umma_commit_elect(bar(L::bVE + st));
         return true;
       };
-      bool ok = wt(bar(L::bQF), 0) && s_of(0) && wt(bar(L::bOF), 0) && dp_of(0);
-      if (ok && n > 1) ok = s_of(1);
-      for (int t = 0; t < n && ok; ++t) {
-        const int st = t % L::kKStages;
+      // acc (+)= A K_t, A the 128 x 128 bf16 operand at `col` (the halves at +0 and +64)
+      auto gather = [&](uint32_t acc, uint32_t col, int ready, int t) -> bool {
+        const uint32_t off = (uint32_t)(t % L::kKStages) * L::kTileBytes;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          ok = ok && wt(bar(L::bDs + g), (uint32_t)t & 1u);
-          if (!ok) break;
+          if (!wt(bar(ready + g), (uint32_t)t & 1u)) return false;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ts_elect(tmem + L::kColQ, tmem + L::kColDp + g * 64 + kk * 8,
-                          dk_t.at((uint32_t)st * L::kTileBytes + (g * 4 + kk) * 16 * 128), idesc_d,
+            umma_ts_elect(tmem + acc, tmem + col + g * 64 + kk * 8,
+                          dk_t.at(off + (g * 4 + kk) * 16 * 128), idesc_d,
                           (t > 0 || g > 0 || kk > 0) ? 1u : 0u);
         }
+        return true;
+      };
+      bool ok = wt(bar(L::bQF), 0) && s_of(0) && wt(bar(L::bOF), 0) && dp_of(0);
+      if (ok && !kFix && n > 1) ok = s_of(1);
+      for (int t = 0; t < n && ok; ++t) {
+        if constexpr (kFix) {
+          ok = gather(L::kColPk, L::kColS, L::bP, t);
+          if (ok && t + 1 < n) ok = s_of(t + 1);
+          if (!ok) break;
+        }
+        ok = gather(L::kColQ, L::kColDp, L::bDs, t);
         if (!ok) break;
-        umma_commit_elect(bar(L::bKE + st));
+        umma_commit_elect(bar(L::bKE + t % L::kKStages));
         if (t + 1 < n) ok = dp_of(t + 1);
         // S(t) was read ahead of dS(t), which has arrived: its buffer is free
-        if (ok && t + 2 < n) ok = s_of(t + 2);
+        if (ok && !kFix && t + 2 < n) ok = s_of(t + 2);
       }
       if (ok) {
         umma_commit_elect(bar(L::bEnd));
@@ -804,22 +841,25 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     const int i = i0 + row;
     const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
     float2 st = make_float2(INFINITY, 0.0f);  // behind the last query: P = 0
-    if (i < m.nq) st = __ldg(p.stat + ((size_t)b * p.s.heads + h) * p.s.q_len + m.q0 + i);
+    const size_t stat_at = ((size_t)b * p.s.heads + h) * p.s.q_len + m.q0 + i;
+    if (i < m.nq) st = p.stat[stat_at];
     const int lim = masked_limit(m, p.s.causal, i);
     const int lim_warp = masked_limit(m, p.s.causal, i0 + wq * 32);
     float slope = 0.0f;
     if constexpr (kBias) slope = __ldg(p.s.slopes + h) * 1.4426950408889634f;
     const float inv_cap = kCap ? 1.0f / p.s.cap_log2 : 0.0f;
     const int place = i + m.nk - m.nq;
+    float2 off2 = make_float2(0.0f, 0.0f);  // e
     bool ok = !*abort_flag;
     for (int t = 0; t < n && ok; ++t) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::bS + (t & 1)), (uint32_t)(t >> 1) & 1u, ctl));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::bS + t % kSBuf), (uint32_t)(t / kSBuf) & 1u,
+                                             ctl));
       if (!ok) break;
       tc_fence_after();
       float s[64];
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        tmem_ld32(trow + L::kColS + 128 * (t & 1) + g * 64 + c * 32,
+        tmem_ld32(trow + L::kColS + 128 * (t % kSBuf) + g * 64 + c * 32,
                   *reinterpret_cast<float(*)[32]>(&s[c * 32]));
       tmem_ld_wait();
       const int kv0 = (begin + t) * kBlockN + g * 64;
@@ -837,7 +877,22 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       for (int c = 0; c < 64; ++c) {
         float a = kCap || kBias ? s[c] - st.x : fmaf(s[c], p.s.scale_log2, -st.x);
         if (masked && kv0 + c >= lim) a = -INFINITY;
-        s[c] = kCap ? ex2(a) * bent[c] : ex2(a);
+        s[c] = ex2(a);
+      }
+      if constexpr (kFix) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            pk[x] = pack_bf16x2(s[c * 32 + 2 * x] * bent[c * 32 + 2 * x],
+                                s[c * 32 + 2 * x + 1] * bent[c * 32 + 2 * x + 1]);
+          tmem_st16(trow + L::kColS + g * 64 + c * 16, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bP + g));
       }
       ok = __all_sync(0xffffffffu, mbar_wait(bar(L::bDp), (uint32_t)t & 1u, ctl));
       if (!ok) break;
@@ -849,9 +904,14 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         tmem_ld_wait();
         uint32_t pk[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          pk[x] = pack_bf16x2(s[c * 32 + 2 * x] * (d[2 * x] - st.y),
-                              s[c * 32 + 2 * x + 1] * (d[2 * x + 1] - st.y));
+        for (int x = 0; x < 16; ++x) {
+          const int q = c * 32 + 2 * x;
+          const float2 r = __fmul2_rn(make_float2(s[q], s[q + 1]),
+                                      __fadd2_rn(make_float2(d[2 * x], d[2 * x + 1]),
+                                                 make_float2(-st.y, -st.y)));
+          off2 = __fadd2_rn(off2, r);
+          pk[x] = kCap ? pack_bf16x2(r.x * bent[q], r.y * bent[q + 1]) : pack_bf16x2(r.x, r.y);
+        }
         tmem_st16(trow + L::kColDp + g * 64 + c * 16, pk);
       }
       tmem_st_wait();
@@ -860,14 +920,31 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       if (lane == 0) mbar_arrive(bar(L::bDs + g));
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::bEnd), 0, ctl));
+    float* sums = reinterpret_cast<float*>(smem + L::kSum);
+    float e = off2.x + off2.y;
+    if (g == 1) sums[row] = e;
     ok = named_bar_and(1, 256, ok && !*abort_flag);
-    if (ok && g == 0) {
+    if (ok) {
       tc_fence_after();
-      const size_t slab =
+      e += g == 0 ? sums[row] : 0.0f;
+      const size_t rows0 =
           (((size_t)part * p.s.batch + b) * p.s.heads + h) * (size_t)p.s.q_len + m.q0;
-      masked_store<D>(trow + L::kColQ, n > 0, p.scale, smem + L::kQ, i0, m.nq,
-                      p.d0 + b * p.stride0[0] + m.q0 * p.stride0[1] + h * p.stride0[2],
-                      p.stride0[1], p.parts > 1 ? p.part0 + slab * D : nullptr);
+      __nv_bfloat16* out = p.d0 + b * p.stride0[0] + m.q0 * p.stride0[1] + h * p.stride0[2];
+      if (p.parts > 1) {
+        // the parts' sums meet in ltx_masked_bwd_sum
+        if (g == 0) {
+          if (i < m.nq) p.part_e[rows0 + i] = e;
+          masked_store<D>(trow + L::kColQ, n > 0, p.scale, smem + L::kQ, i0, m.nq, out,
+                          p.stride0[1], p.part0 + rows0 * D);
+        } else if (kFix) {
+          masked_store<D>(trow + L::kColPk, n > 0, p.scale, smem + L::kQ, i0, m.nq, out,
+                          p.stride0[1], p.part1 + rows0 * D);
+        }
+      } else if (g == 0) {
+        if (i < m.nq) p.stat[stat_at].y = st.y + e;
+        masked_store<D>(trow + L::kColQ, n > 0, p.scale, smem + L::kQ, i0, m.nq, out,
+                        p.stride0[1], nullptr, kFix ? trow + L::kColPk : 0u, e);
+      }
     }
   }
 
@@ -881,12 +958,15 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 }
 
 // Sum of the fp32 partials of one gradient, in a fixed order, rounded to bf16.  One thread per
-// 4 channels; rows of no document are left as they are.
+// 4 channels; rows of no document are left as they are.  part_e (dQ): the parts' e, whose sum
+// goes into stat, and with part_fix takes that many times the sum of its partials off.
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
-    ltx_masked_bwd_sum(const float* __restrict__ part, __nv_bfloat16* __restrict__ out, int parts,
-                       int batch, int heads, int len, const int* __restrict__ starts, int docs,
-                       long long sb, long long sl, long long sh) {
+    ltx_masked_bwd_sum(const float* __restrict__ part, const float* __restrict__ part_fix,
+                       const float* __restrict__ part_e, float2* __restrict__ stat,
+                       __nv_bfloat16* __restrict__ out, int parts, int batch, int heads, int len,
+                       const int* __restrict__ starts, int docs, long long sb, long long sl,
+                       long long sh) {
   constexpr int kVec = D / 4;
   const long long tid = (long long)blockIdx.x * kCombineThreads + threadIdx.x;
   const long long rows = (long long)batch * heads * len;
@@ -905,6 +985,20 @@ __global__ void __launch_bounds__(kCombineThreads)
     a.y += v.y;
     a.z += v.z;
     a.w += v.w;
+  }
+  if (part_e) {
+    float e = 0.0f;
+    for (int x = 0; x < parts; ++x) e += part_e[x * rows + row];
+    if (part_fix) {
+      for (int x = 0; x < parts; ++x) {
+        const float4 v = reinterpret_cast<const float4*>(part_fix + (x * rows + row) * D)[c];
+        a.x = fmaf(-e, v.x, a.x);
+        a.y = fmaf(-e, v.y, a.y);
+        a.z = fmaf(-e, v.z, a.z);
+        a.w = fmaf(-e, v.w, a.w);
+      }
+    }
+    if (c == 0) stat[row].y += e;
   }
   *reinterpret_cast<uint2*>(out + b * sb + i * sl + h * sh + c * 4) =
       make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));

@@ -93,47 +93,76 @@ __device__ __forceinline__ void masked_range(const int* starts, int d, int len, 
   n = max(min(max(__ldg(starts + d + 1), 0), len) - first, 0);
 }
 
+// Where a CTA of a grid of (unit, batch row, part, head) works, heads fastest: CTAs start in
+// the order of their index, so the units are numbered with the longest first (masked_find) and
+// every head's longest ones run ahead of anybody's shorter ones.
+struct MaskedPlace {
+  int unit, b, part, head;
+};
+
+__device__ __forceinline__ MaskedPlace masked_place(int heads, int batch, int parts) {
+  unsigned x = blockIdx.x;
+  MaskedPlace w;
+  w.head = (int)(x % (unsigned)heads);
+  x /= (unsigned)heads;
+  w.part = (int)(x % (unsigned)parts);
+  x /= (unsigned)parts;
+  w.b = (int)(x % (unsigned)batch);
+  w.unit = (int)(x / (unsigned)batch);
+  return w;
+}
+
 // Unit `unit` of batch row b when every document is cut into units of `rows` rows of its
-// queries (kKeys: of its keys).  Whole warp.
+// queries (kKeys: of its keys).  Up to 32 documents are taken in the order of their units'
+// work (the other axis's length), the longest first, more in their own order; within a causal
+// document the later queries, which see more, come first.  Whole warp.
 template <bool kKeys>
 __device__ __forceinline__ MaskedDoc masked_find(const MaskedShape& s, int b, int unit,
                                                  int rows) {
   const int lane = threadIdx.x & 31;
   MaskedDoc m;
   m.tile = -1;
+  auto nth = [&](int n, int tiles) { return !kKeys && s.causal ? tiles - 1 - n : n; };
   if (s.docs == 0) {
     m.q0 = m.k0 = 0;
     m.nq = s.q_len;
     m.nk = s.kv_len;
     m.prefix = s.prefix ? __ldg(s.prefix + b) : 0;
-    if ((long long)unit * rows < (kKeys ? m.nk : m.nq)) m.tile = unit;
+    const int tiles = ((kKeys ? m.nk : m.nq) + rows - 1) / rows;
+    if (unit < tiles) m.tile = nth(unit, tiles);
     return m;
   }
   const int* qs = s.q_starts + (size_t)b * (s.docs + 1);
   const int* ks = s.kv_starts + (size_t)b * (s.docs + 1);
   for (int d0 = 0; d0 < s.docs; d0 += 32) {
-    int first = 0, n = 0;
-    if (d0 + lane < s.docs)
-      masked_range(kKeys ? ks : qs, d0 + lane, kKeys ? s.kv_len : s.q_len, first, n);
-    const int tiles = (n + rows - 1) / rows;
-    int end = tiles;  // inclusive scan
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, end, off);
-      if (lane >= off) end += x;
+    const int d = d0 + lane;
+    int q0 = 0, nq = 0, k0 = 0, nk = 0, prefix = 0;
+    if (d < s.docs) {
+      masked_range(qs, d, s.q_len, q0, nq);
+      masked_range(ks, d, s.kv_len, k0, nk);
+      if (s.prefix) prefix = __ldg(s.prefix + (size_t)b * s.docs + d);
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, end > unit);
+    const int tiles = ((kKeys ? nk : nq) + rows - 1) / rows;
+    const int weight = s.docs <= 32 ? (kKeys ? nq : nk) : 0;
+    const int here = min(s.docs - d0, 32);
+    int end = 0;  // units up to and with this document's
+    for (int x = 0; x < here; ++x) {
+      const int wx = __shfl_sync(0xffffffffu, weight, x), tx = __shfl_sync(0xffffffffu, tiles, x);
+      if (wx > weight || (wx == weight && x <= lane)) end += tx;
+    }
+    const uint32_t hit =
+        __ballot_sync(0xffffffffu, lane < here && end - tiles <= unit && unit < end);
     if (hit) {
       const int at = __ffs(hit) - 1;
-      const int before = __shfl_sync(0xffffffffu, end - tiles, at);
-      const int d = d0 + at;
-      masked_range(qs, d, s.q_len, m.q0, m.nq);
-      masked_range(ks, d, s.kv_len, m.k0, m.nk);
-      m.prefix = s.prefix ? __ldg(s.prefix + (size_t)b * s.docs + d) : 0;
-      m.tile = unit - before;
+      m.q0 = __shfl_sync(0xffffffffu, q0, at);
+      m.nq = __shfl_sync(0xffffffffu, nq, at);
+      m.k0 = __shfl_sync(0xffffffffu, k0, at);
+      m.nk = __shfl_sync(0xffffffffu, nk, at);
+      m.prefix = __shfl_sync(0xffffffffu, prefix, at);
+      m.tile = __shfl_sync(0xffffffffu, nth(unit - (end - tiles), tiles), at);
       return m;
     }
-    unit -= __shfl_sync(0xffffffffu, end, 31);
+    unit -= __reduce_add_sync(0xffffffffu, tiles);
   }
   return m;
 }
@@ -282,19 +311,17 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int hy = blockIdx.y;  // key head when heads are packed, else query head
-  const int b = (int)blockIdx.z / p.parts;
-  const int part = (int)blockIdx.z % p.parts;
   const int pack = p.s.pack;
+  const MaskedPlace at_work = masked_place(p.s.heads / pack, p.s.batch, p.parts);
+  const int hy = at_work.head;  // key head when heads are packed, else query head
+  const int b = at_work.b, part = at_work.part;
   const int tile_tokens = kBlockM / pack;
   const int h0 = hy * pack;                            // first query head of the rows
   const int hk = pack > 1 ? hy : hy / p.s.group;       // key head
 
   if (warp == 2) {
-    // causal units grow with their index: the longest first
-    const int unit = p.s.causal ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
     const MaskedDoc m =
-        masked_find<false>(p.s, b, unit, tile_tokens * L::kQTiles);
+        masked_find<false>(p.s, b, at_work.unit, tile_tokens * L::kQTiles);
     if (lane == 0) *shared_doc = m;
   }
   if (threadIdx.x == 0) {

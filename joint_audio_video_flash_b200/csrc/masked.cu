@@ -15,6 +15,7 @@ using ltx::ranges_overlap;
 
 constexpr unsigned long long kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr long long kMaxCtas = 0x7fffffffLL;  // of a one-dimensional grid
 
 // A [batch, len, heads, head_dim] bf16 tensor with strides in elements; a stride counts only
 // where there is a second row to step to.
@@ -180,6 +181,10 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
   return s;
 }
 
+long long grid_ctas(int units, int heads, int batch, int parts) {
+  return (long long)units * heads * batch * parts;
+}
+
 struct FwdPlan {
   bool alt;    // one query tile per CTA, accumulators on alternate key tiles
   int units;   // CTAs along the queries of one (batch row, head): an upper bound
@@ -226,8 +231,7 @@ size_t partial_bytes(const ltx::MaskedShape& s, int head_dim, int parts) {
 template <int D, bool kAlt, bool kCap, bool kBias>
 cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const ltx::MaskedFwdParams& p, int units, cudaStream_t stream) {
-  const dim3 grid((unsigned)units, (unsigned)(p.s.heads / p.s.pack),
-                  (unsigned)(p.s.batch * p.parts));
+  const unsigned grid = (unsigned)grid_ctas(units, p.s.heads / p.s.pack, p.s.batch, p.parts);
   ltx::ltx_masked_fwd<D, kAlt, kCap, kBias>
       <<<grid, ltx::kMaskedThreads, ltx::MaskedSmem<D, kAlt>::kAlloc, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
@@ -268,7 +272,8 @@ struct BwdPlan {
   size_t stat, partials;  // bytes of workspace
 };
 
-BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, int num_sms) {
+// cap: dQ's parts carry the second accumulator too.
+BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, bool cap, int num_sms) {
   BwdPlan f;
   const long long docs = std::max(s.docs, 1);
   const int kt = (s.kv_len + ltx::kBlockN - 1) / ltx::kBlockN;
@@ -285,7 +290,9 @@ BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, int num_sms) {
   const size_t row = (size_t)head_dim * sizeof(float);
   const size_t kv = f.parts_kv > 1
                         ? 2 * (size_t)f.parts_kv * s.batch * s.kv_heads * s.kv_len * row : 0;
-  const size_t q = f.parts_q > 1 ? (size_t)f.parts_q * s.batch * s.heads * s.q_len * row : 0;
+  const size_t q = f.parts_q > 1 ? (size_t)f.parts_q * s.batch * s.heads * s.q_len *
+                                       ((cap ? 2 : 1) * row + sizeof(float))
+                                 : 0;
   f.partials = std::max(kv, q);  // used one after the other
   return f;
 }
@@ -297,7 +304,7 @@ struct BwdMaps {
 template <int D, bool kCap, bool kBias>
 cudaError_t launch_kv(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
                       cudaStream_t stream) {
-  const dim3 grid((unsigned)units, (unsigned)p.s.kv_heads, (unsigned)(p.s.batch * p.parts));
+  const unsigned grid = (unsigned)grid_ctas(units, p.s.kv_heads, p.s.batch, p.parts);
   ltx::ltx_masked_bwd_kv<D, kCap, kBias>
       <<<grid, ltx::kMaskedThreads, ltx::BwdKvSmem<D>::kAlloc, stream>>>(t.q, t.k, t.v, t.d_out,
                                                                          p);
@@ -307,19 +314,21 @@ cudaError_t launch_kv(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units
 template <int D, bool kCap, bool kBias>
 cudaError_t launch_q(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
                      cudaStream_t stream) {
-  const dim3 grid((unsigned)units, (unsigned)p.s.heads, (unsigned)(p.s.batch * p.parts));
+  const unsigned grid = (unsigned)grid_ctas(units, p.s.heads, p.s.batch, p.parts);
   ltx::ltx_masked_bwd_q<D, kCap, kBias>
-      <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D>::kAlloc, stream>>>(t.q, t.k, t.v, t.d_out, p);
+      <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D, kCap>::kAlloc, stream>>>(t.q, t.k, t.v, t.d_out, p);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_sum(const float* part, const Tensor& out, int parts, const int* starts,
-                       int docs, cudaStream_t stream) {
+cudaError_t launch_sum(const ltx::MaskedBwdParams& p, const float* part, const float* fix,
+                       const float* e, const Tensor& out, const int* starts, int docs,
+                       cudaStream_t stream) {
   const long long n = out.batch * out.heads * out.len * (D / 4);
   ltx::ltx_masked_bwd_sum<D>
       <<<(unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads), ltx::kCombineThreads,
-         0, stream>>>(part, static_cast<__nv_bfloat16*>(const_cast<void*>(out.base)), parts,
+         0, stream>>>(part, fix, e, p.stat,
+                      static_cast<__nv_bfloat16*>(const_cast<void*>(out.base)), p.parts,
                       (int)out.batch, (int)out.heads, (int)out.len, starts, docs, out.sb, out.sl,
                       out.sh);
   return cudaGetLastError();
@@ -342,15 +351,32 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
               (unsigned)a.batch),
          256, 0, stream>>>(static_cast<const __nv_bfloat16*>(t.out.base),
                            static_cast<const __nv_bfloat16*>(d_out.base), a.lse,
-                           const_cast<float2*>(p.stat), a.heads, a.q_len, t.out.sb, t.out.sl,
+                           p.stat, a.heads, a.q_len, t.out.sb, t.out.sl,
                            t.out.sh, d_out.sb, d_out.sl, d_out.sh);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const bool cap = a.softcap > 0.0f, bias = a.slopes != nullptr;
+  // dQ first: it leaves delta free of out's rounding
+  p.parts = f.parts_q;
+  set_target(dq, &p.d0, p.stride0);
+  if (p.parts > 1) {
+    const size_t rows = (size_t)p.parts * a.batch * a.heads * a.q_len;
+    p.part0 = partials;
+    p.part1 = cap ? partials + rows * D : nullptr;
+    p.part_e = partials + rows * D * (cap ? 2 : 1);
+  }
+  e = cap ? (bias ? launch_q<D, true, true>(maps, p, f.units_q, stream)
+                  : launch_q<D, true, false>(maps, p, f.units_q, stream))
+          : (bias ? launch_q<D, false, true>(maps, p, f.units_q, stream)
+                  : launch_q<D, false, false>(maps, p, f.units_q, stream));
+  if (e == cudaSuccess && p.parts > 1)
+    e = launch_sum<D>(p, p.part0, p.part1, p.part_e, dq, a.q_starts, a.docs, stream);
+  if (e != cudaSuccess) return e;
   // dK and dV
   p.parts = f.parts_kv;
   set_target(dk, &p.d0, p.stride0);
   set_target(dv, &p.d1, p.stride1);
+  p.part0 = p.part1 = p.part_e = nullptr;
   if (p.parts > 1) {
     p.part0 = partials;
     p.part1 = partials + (size_t)p.parts * a.batch * a.kv_heads * a.kv_len * D;
@@ -360,21 +386,10 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
           : (bias ? launch_kv<D, false, true>(maps, p, f.units_kv, stream)
                   : launch_kv<D, false, false>(maps, p, f.units_kv, stream));
   if (e == cudaSuccess && p.parts > 1) {
-    e = launch_sum<D>(p.part0, dk, p.parts, a.kv_starts, a.docs, stream);
-    if (e == cudaSuccess) e = launch_sum<D>(p.part1, dv, p.parts, a.kv_starts, a.docs, stream);
+    e = launch_sum<D>(p, p.part0, nullptr, nullptr, dk, a.kv_starts, a.docs, stream);
+    if (e == cudaSuccess)
+      e = launch_sum<D>(p, p.part1, nullptr, nullptr, dv, a.kv_starts, a.docs, stream);
   }
-  if (e != cudaSuccess) return e;
-  // dQ
-  p.parts = f.parts_q;
-  set_target(dq, &p.d0, p.stride0);
-  p.part0 = p.parts > 1 ? partials : nullptr;
-  p.part1 = nullptr;
-  e = cap ? (bias ? launch_q<D, true, true>(maps, p, f.units_q, stream)
-                  : launch_q<D, true, false>(maps, p, f.units_q, stream))
-          : (bias ? launch_q<D, false, true>(maps, p, f.units_q, stream)
-                  : launch_q<D, false, false>(maps, p, f.units_q, stream));
-  if (e == cudaSuccess && p.parts > 1)
-    e = launch_sum<D>(p.part0, dq, p.parts, a.q_starts, a.docs, stream);
   return e;
 }
 
@@ -386,7 +401,7 @@ cudaError_t set_bwd() {
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, kCap, kBias>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ltx::BwdQSmem<D>::kAlloc);
+                              ltx::BwdQSmem<D, kCap>::kAlloc);
 }
 
 template <int D>
@@ -442,7 +457,7 @@ int ltxattn_masked_workspace(const ltxattn_masked_call* call, int backward,
   if (err != LTXATTN_OK) return err;
   const ltx::MaskedShape s = shape_of(*call, c);
   if (backward) {
-    const BwdPlan f = plan_backward(s, call->head_dim, c.num_sms);
+    const BwdPlan f = plan_backward(s, call->head_dim, call->softcap > 0.0f, c.num_sms);
     *bytes = f.stat + f.partials;
   } else {
     *bytes = partial_bytes(s, call->head_dim, plan_forward(s, c.num_sms).parts);
@@ -478,7 +493,8 @@ int ltxattn_masked_forward(const ltxattn_masked_call* call, void* workspace,
   p.lse = a.lse;
   const FwdPlan f = plan_forward(p.s, c.num_sms);
   p.parts = f.parts;
-  if ((long long)a.batch * f.parts > 65535) return LTXATTN_ERR_UNSUPPORTED;
+  if (grid_ctas(f.units, a.heads / p.s.pack, a.batch, f.parts) > kMaxCtas)
+    return LTXATTN_ERR_UNSUPPORTED;
   const size_t need = partial_bytes(p.s, a.head_dim, f.parts);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return LTXATTN_ERR_INVALID_ARG;
@@ -543,8 +559,10 @@ int ltxattn_masked_backward(const ltxattn_masked_call* call, const ltxattn_maske
   p.s = shape_of(a, c);
   p.s.pack = 1;
   p.scale = a.scale;
-  const BwdPlan f = plan_backward(p.s, d, c.num_sms);
-  if ((long long)a.batch * std::max(f.parts_kv, f.parts_q) > 65535) return LTXATTN_ERR_UNSUPPORTED;
+  const BwdPlan f = plan_backward(p.s, d, a.softcap > 0.0f, c.num_sms);
+  if (grid_ctas(f.units_kv, a.kv_heads, a.batch, f.parts_kv) > kMaxCtas ||
+      grid_ctas(f.units_q, a.heads, a.batch, f.parts_q) > kMaxCtas)
+    return LTXATTN_ERR_UNSUPPORTED;
   const size_t need = f.stat + f.partials;
   if (!workspace || workspace_bytes < need) return LTXATTN_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) & 15u) return LTXATTN_ERR_MISALIGNED;
@@ -555,7 +573,7 @@ int ltxattn_masked_backward(const ltxattn_masked_call* call, const ltxattn_maske
   if (overlaps_small(a, workspace, need) ||
       ranges_overlap(workspace, need, a.lse, lse_bytes(a)))
     return LTXATTN_ERR_INVALID_ARG;
-  p.stat = static_cast<const float2*>(workspace);
+  p.stat = static_cast<float2*>(workspace);
   float* partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + f.stat);
   BwdMaps maps;
   if (!encode(c, &maps.q, t.q, ltx::kBlockM, 1) || !encode(c, &maps.k, t.k, ltx::kBlockN, 1) ||
