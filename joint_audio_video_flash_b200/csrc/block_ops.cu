@@ -55,19 +55,20 @@ bool views_apart(const View& a, const View& b) {
 
 template <typename T, bool kHalves>
 int launch_rope(ltx::RopeParams& p, cudaStream_t stream) {
-  const int resident = ltx::resident_ctas<ltx::ltx_rope_axes<T, kHalves>>(ltx::kRopeThreads);
+  using L = ltx::RopeShape<T, kHalves>;
+  const int resident =
+      ltx::resident_ctas<ltx::ltx_rope_axes<T, kHalves>>(ltx::kRopeThreads, L::kSmem);
   if (resident < 1) return LTXATTN_ERR_CUDA;
-  constexpr int kChunk = ltx::Elem<T>::kVec, kHeads = ltx::kRopeHeads / (kHalves ? 2 : 1);
-  p.units = p.head_dim / (kHalves ? 2 * kChunk : kChunk);
+  p.units = p.head_dim / (L::kParts * L::V);
   const int slots = ltx::kRopeThreads / p.units;  // units <= 128
   // as few threads to a token as still hold its heads, so that every thread has its full step
-  p.head_slots = std::min((p.heads + kHeads - 1) / kHeads, slots);
+  p.head_slots = std::min((p.heads + L::kHeads - 1) / L::kHeads, slots);
   p.tokens = slots / p.head_slots;
-  p.steps = (p.heads + p.head_slots * kHeads - 1) / (p.head_slots * kHeads);
+  p.steps = (p.heads + p.head_slots * L::kHeads - 1) / (p.head_slots * L::kHeads);
   const long long rows = (long long)p.batch * p.len;
   const unsigned grid =
       (unsigned)std::min<long long>((rows + p.tokens - 1) / p.tokens, resident);
-  ltx::ltx_rope_axes<T, kHalves><<<grid, ltx::kRopeThreads, 0, stream>>>(p);
+  ltx::ltx_rope_axes<T, kHalves><<<grid, ltx::kRopeThreads, L::kSmem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
 }
 

@@ -23,10 +23,11 @@ inline bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
-// CTAs of `kernel` (no dynamic shared memory) that the current device holds at once, looked
-// up once per device; 0 when a CUDA call failed.
+// CTAs of `kernel` with `smem` bytes of dynamic shared memory (always the same for a kernel)
+// that the current device holds at once, looked up, and the kernel's limit set, once per
+// device; 0 when a CUDA call failed.
 template <auto kernel>
-int resident_ctas(int threads) {
+int resident_ctas(int threads, int smem = 0) {
   constexpr int kMaxDevices = 64;
   static std::mutex mu;
   static int resident[kMaxDevices];
@@ -39,7 +40,10 @@ int resident_ctas(int threads) {
   if (resident[dev] == 0) {
     int sms = 0, per_sm = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) !=
+        (smem > 48 * 1024 &&
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+             cudaSuccess) ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) !=
             cudaSuccess) {
       cudaGetLastError();
       return 0;

@@ -10,16 +10,17 @@
 // so angles never exist in fp32.  freq comes in turns (1 / 2 pi radians) as a pair of floats
 // (hi + lo, 48 bits); the product with the fp32 position is split into its rounded value and
 // its exact remainder (one fused multiply-add), whole turns are dropped from each part, and
-// sincospif takes the fraction.
+// sine and cosine are taken of the fraction.
 //
-// Bound by HBM: q and k are read and written once and nothing else moves; what it takes is few
-// instructions per chunk.  Persistent CTAs walk tokens.  A thread owns one 16-byte chunk
-// position of a head (two, half a head apart, in the split layout) and up to four heads of a
-// token; the sines and cosines of a token are computed once per CTA, an entry a thread, into
-// shared memory, and read back per chunk position.  The chunks and positions of the next step
-// are loaded ahead of the arithmetic of this one (two register sets, two tables, one barrier a
-// step).  15360 tokens x 64 heads x 128 bf16: 107 us (4.7 TB/s); with every thread computing the
-// sines of its own pairs (16 times as many of them) it took 124 us.
+// Bound by HBM: q and k are read and written once and nothing else moves, so what counts is
+// bytes in flight and few instructions per chunk.  Persistent CTAs walk tokens.  A thread owns
+// one 16-byte chunk position of a head (two, half a head apart, in the split layout) and up to
+// four chunks of a step; it copies them asynchronously into slots of its own in shared memory,
+// kStages - 1 steps ahead, so that no register holds them and no thread waits for another's
+// data.  The sines and cosines of a token are computed once per CTA, an entry a thread, into a
+// table that every thread reads (two tables, one barrier a step).  15360 tokens x 64 heads x 128
+// bf16: 80 us (6.3 TB/s); with the next step's chunks in registers instead 107 us, with every
+// thread computing the sines of its own pairs (16 times as many of them) 124 us.
 #pragma once
 
 #include "dtype.cuh"
@@ -30,7 +31,7 @@ namespace ltx {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxPairs = 256;  // head_dim <= 512
 constexpr int kRopeMaxAxes = 4;
-constexpr int kRopeHeads = 4;    // heads of a thread's step (2 in the split layout)
+constexpr int kRopeChunks = 4;   // chunks of a thread's step
 
 struct RopeParams {
   const void* x[2];      // q, k
@@ -75,14 +76,30 @@ __device__ __forceinline__ void sincos_turns(float turns, float& s, float& c) {
 }
 
 template <typename T, bool kHalves>
+struct RopeShape {
+  static constexpr int V = Elem<T>::kVec;
+  static constexpr int kPairs = kHalves ? V : V / 2;  // pairs a thread owns
+  static constexpr int kParts = kHalves ? 2 : 1;      // chunks of a head it owns
+  static constexpr int kHeads = kRopeChunks / kParts;  // heads of its step
+  static constexpr int kStages = kPairs == 8 ? 3 : 4;  // two CTAs share an SM's memory
+  // [stages][chunks][threads] 16 bytes, then [stages][pairs][threads] positions, then
+  // [2 tables][cos, sin][pairs * threads]
+  static constexpr int kPos = kStages * kRopeChunks * kRopeThreads * 16;
+  static constexpr int kTable = kPos + kStages * kPairs * kRopeThreads * 4;
+  static constexpr int kSmem = kTable + 4 * kPairs * kRopeThreads * 4;
+  static_assert(2 * (kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
+};
+
+template <typename T, bool kHalves>
 __global__ void __launch_bounds__(kRopeThreads, 2)
     ltx_rope_axes(const __grid_constant__ RopeParams p) {
-  constexpr int V = Elem<T>::kVec;
-  constexpr int kPairs = kHalves ? V : V / 2;  // pairs a thread owns
-  constexpr int kParts = kHalves ? 2 : 1;      // chunks of a head it owns
-  constexpr int kHeads = kRopeHeads / kParts;
-  // [2 tables][cos, sin][tokens * head_dim / 2], at most kPairs entries a thread
-  __shared__ __align__(16) float table[2][2][kPairs * kRopeThreads];
+  using L = RopeShape<T, kHalves>;
+  constexpr int V = L::V, kPairs = L::kPairs, kParts = L::kParts, kHeads = L::kHeads;
+  constexpr int kStages = L::kStages, kEntries = kPairs * kRopeThreads;
+  extern __shared__ __align__(16) unsigned char smem[];
+  uint4* chunks = reinterpret_cast<uint4*>(smem) + threadIdx.x;
+  float* pos = reinterpret_cast<float*>(smem + L::kPos) + threadIdx.x;
+  float* table = reinterpret_cast<float*>(smem + L::kTable);
   const int slot = threadIdx.x / p.units, unit = threadIdx.x % p.units;
   const int local = slot / p.head_slots, h0 = slot % p.head_slots;
   const int half = p.head_dim / 2;
@@ -104,150 +121,18 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
 #pragma unroll
     for (int a = 0; a + 1 < kRopeMaxAxes; ++a)
       axis[i] += (a + 1 < p.axes && pair >= p.axis_end[a]);
-    if (!turned) axis[i] = -1;  // position 0: cos 1, sin 0
-  }
-  // heads of a token's first step: where they lie within it, and whether they are keys
-  const T* src0[kHeads];
-  T* dst0[kHeads];
-  bool key0[kHeads];
-#pragma unroll
-  for (int u = 0; u < kHeads; ++u) {
-    const int h = h0 + u * p.head_slots, k = h >= p.heads_q;
-    const long long at = h - (k ? p.heads_q : 0);
-    key0[u] = k;
-    src0[u] = static_cast<const T*>(p.x[k]) + at * p.x_stride[k][2] + e0;
-    dst0[u] = static_cast<T*>(p.out[k]) + at * p.out_stride[k][2] + e0;
+    if (!turned) axis[i] = -1;  // turns by nothing: cos 1, sin 0
   }
 
-  // batch row and place of token `n` behind the step's first one, (b, l)
-  auto place = [&](int& b, int& l, int n) {
-    l += n;
-    if (l >= p.len) {
-      b += l / p.len;
-      l %= p.len;
-    }
-  };
-  struct Step {
-    uint4 v[kHeads][kParts];
-    float x[kPairs];  // positions of the entries (a token's first step)
-    int b, l;
-  };
-  // (b0, l0): the step's first token, number `base`
-  auto load = [&](Step& st, uint32_t base, int b0, int l0, int step) {
-    if (step == 0) {
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        st.x[i] = 0.0f;
-        if (axis[i] >= 0 && base + (uint32_t)entry_token[i] < rows) {
-          int b = b0, l = l0;
-          place(b, l, entry_token[i]);
-          st.x[i] = __ldg(p.positions + b * p.pos_batch + (long long)l * p.axes + axis[i]);
-        }
-      }
-    }
-    if (!owner || base + (uint32_t)local >= rows) return;
-    st.b = b0;
-    st.l = l0;
-    place(st.b, st.l, local);
-    const long long off[2] = {st.b * p.x_stride[0][0] + st.l * p.x_stride[0][1],
-                              st.b * p.x_stride[1][0] + st.l * p.x_stride[1][1]};
-#pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      const int h = h0 + (step * kHeads + u) * p.head_slots;
-      if (h >= p.heads) break;
-      const T* s = src0[u];
-      bool k = key0[u];
-      if (step != 0) {
-        k = h >= p.heads_q;
-        s = static_cast<const T*>(k ? p.x[1] : p.x[0]) +
-            (long long)(h - (k ? p.heads_q : 0)) * (k ? p.x_stride[1][2] : p.x_stride[0][2]) + e0;
-      }
-      s += k ? off[1] : off[0];
-#pragma unroll
-      for (int y = 0; y < kParts; ++y)
-        st.v[u][y] = __ldcs(reinterpret_cast<const uint4*>(s + y * half));
-    }
-  };
-  // the table of a step's tokens
-  auto fill = [&](const Step& st, int which) {
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const int entry = i * kRopeThreads + (int)threadIdx.x;
-      if (entry >= p.tokens * half) break;
-      const float whole = st.x[i] * freq[i].x;
-      float rest = fmaf(st.x[i], freq[i].y, fmaf(st.x[i], freq[i].x, -whole));
-      rest -= rintf(rest);
-      float sn, cs;
-      sincos_turns((whole - rintf(whole)) + rest, sn, cs);
-      table[which][0][entry] = cs;
-      table[which][1][entry] = sn * p.sign;
-    }
-  };
-  float2 c[kPairs / 2], s[kPairs / 2];
-  auto turn = [&](const Step& st, uint32_t base, int step, int which) {
-    if (!owner || base + (uint32_t)local >= rows) return;
-    if (step == 0) {
-      const int at = local * half + (kHalves ? e0 : e0 / 2);
-#pragma unroll
-      for (int i = 0; i < kPairs / 2; ++i) {
-        c[i] = *reinterpret_cast<const float2*>(&table[which][0][at + 2 * i]);
-        s[i] = *reinterpret_cast<const float2*>(&table[which][1][at + 2 * i]);
-      }
-    }
-    const long long off[2] = {st.b * p.out_stride[0][0] + st.l * p.out_stride[0][1],
-                              st.b * p.out_stride[1][0] + st.l * p.out_stride[1][1]};
-#pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-      const int h = h0 + (step * kHeads + u) * p.head_slots;
-      if (h >= p.heads) break;
-      T* o = dst0[u];
-      bool k = key0[u];
-      if (step != 0) {
-        k = h >= p.heads_q;
-        o = static_cast<T*>(k ? p.out[1] : p.out[0]) +
-            (long long)(h - (k ? p.heads_q : 0)) * (k ? p.out_stride[1][2] : p.out_stride[0][2]) +
-            e0;
-      }
-      o += k ? off[1] : off[0];
-      float x[V], y[V];
-      Elem<T>::unpack(st.v[u][0], x);
-      if constexpr (kHalves) {
-        float z[V], w[V];
-        Elem<T>::unpack(st.v[u][1], z);
-#pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float2 xi = make_float2(x[i], x[i + 1]), zi = make_float2(z[i], z[i + 1]);
-          const float2 ns = make_float2(-s[i / 2].x, -s[i / 2].y);
-          const float2 a = __ffma2_rn(xi, c[i / 2], __fmul2_rn(zi, ns));
-          const float2 b = __ffma2_rn(xi, s[i / 2], __fmul2_rn(zi, c[i / 2]));
-          y[i] = a.x, y[i + 1] = a.y;
-          w[i] = b.x, w[i + 1] = b.y;
-        }
-        __stcs(reinterpret_cast<uint4*>(o), Elem<T>::pack(y));
-        __stcs(reinterpret_cast<uint4*>(o + half), Elem<T>::pack(w));
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {  // two pairs at once
-          const float2 xi = make_float2(x[i], x[i + 2]), zi = make_float2(x[i + 1], x[i + 3]);
-          const float2 ns = make_float2(-s[i / 4].x, -s[i / 4].y);
-          const float2 a = __ffma2_rn(xi, c[i / 4], __fmul2_rn(zi, ns));
-          const float2 b = __ffma2_rn(xi, s[i / 4], __fmul2_rn(zi, c[i / 4]));
-          y[i] = a.x, y[i + 2] = a.y;
-          y[i + 1] = b.x, y[i + 3] = b.y;
-        }
-        __stcs(reinterpret_cast<uint4*>(o), Elem<T>::pack(y));
-      }
-    }
-  };
-  // (token, step) of this CTA, the same in all its threads.  In place, a thread reads only
-  // chunks that it writes itself and writes them later, so loading ahead is safe
-  const uint32_t stride = gridDim.x * (uint32_t)p.tokens;
-  const int stride_b = (int)(stride / (uint32_t)p.len), stride_l = (int)(stride % (uint32_t)p.len);
+  // A step: tokens base, base + 1, ... (p.tokens of them), of which (b, l) is the first, and
+  // one of the p.steps stretches of their heads.
   struct At {
     uint32_t base;
     int b, l, step;
   };
-  auto next = [&](At at) {
+  const uint32_t stride = gridDim.x * (uint32_t)p.tokens;
+  const int stride_b = (int)(stride / (uint32_t)p.len), stride_l = (int)(stride % (uint32_t)p.len);
+  auto next = [&](At& at) {
     if (++at.step == p.steps) {
       at.step = 0;
       at.base += stride;
@@ -258,30 +143,145 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
         ++at.b;
       }
     }
-    return at;
   };
-  At at0{blockIdx.x * (uint32_t)p.tokens, 0, 0, 0};
-  at0.b = (int)(at0.base / (uint32_t)p.len);
-  at0.l = (int)(at0.base % (uint32_t)p.len);
-  int which = 0;
-  Step a, b;
-  load(a, at0.base, at0.b, at0.l, 0);
-  fill(a, which);
+  // batch row and place of the n-th token of a step
+  auto place = [&](const At& at, int n, int& b, int& l) {
+    b = at.b;
+    l = at.l + n;
+    if (l >= p.len) {
+      b += l / p.len;
+      l %= p.len;
+    }
+  };
+  // starts the copies of a step into stage `st` (always one group, maybe an empty one)
+  auto load = [&](const At& at, int st) {
+    if (at.step == 0 && at.base < rows) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        if (axis[i] >= 0 && at.base + (uint32_t)entry_token[i] < rows) {
+          int b, l;
+          place(at, entry_token[i], b, l);
+          cp_async4(pos + (st * kPairs + i) * kRopeThreads,
+                    p.positions + b * p.pos_batch + (long long)l * p.axes + axis[i]);
+        }
+      }
+    }
+    if (owner && at.base + (uint32_t)local < rows) {
+      int b, l;
+      place(at, local, b, l);
+      const T* x0 = static_cast<const T*>(p.x[0]) + b * p.x_stride[0][0] + l * p.x_stride[0][1] + e0;
+      const T* x1 = static_cast<const T*>(p.x[1]) + b * p.x_stride[1][0] + l * p.x_stride[1][1] + e0;
+#pragma unroll
+      for (int u = 0; u < kHeads; ++u) {
+        const int h = h0 + (at.step * kHeads + u) * p.head_slots;
+        if (h < p.heads) {
+          const T* s = h < p.heads_q ? x0 + h * p.x_stride[0][2]
+                                     : x1 + (h - p.heads_q) * p.x_stride[1][2];
+#pragma unroll
+          for (int y = 0; y < kParts; ++y)
+            cp_async16(chunks + (st * kRopeChunks + u * kParts + y) * kRopeThreads, s + y * half);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  // the table of a step's tokens
+  auto fill = [&](const At& at, int st, int which) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int entry = i * kRopeThreads + (int)threadIdx.x;
+      if (entry >= p.tokens * half) break;
+      float x = 0.0f;
+      if (axis[i] >= 0 && at.base + (uint32_t)entry_token[i] < rows)
+        x = pos[(st * kPairs + i) * kRopeThreads];
+      const float whole = x * freq[i].x;
+      float rest = fmaf(x, freq[i].y, fmaf(x, freq[i].x, -whole));
+      rest -= rintf(rest);
+      float sn, cs;
+      sincos_turns((whole - rintf(whole)) + rest, sn, cs);
+      table[which * 2 * kEntries + entry] = cs;
+      table[(which * 2 + 1) * kEntries + entry] = sn * p.sign;
+    }
+  };
+  float2 c[kPairs / 2], s[kPairs / 2];
+  auto turn = [&](const At& at, int st, int which) {
+    if (!owner || at.base + (uint32_t)local >= rows) return;
+    if (at.step == 0) {
+      const float* t = table + which * 2 * kEntries + local * half + (kHalves ? e0 : e0 / 2);
+#pragma unroll
+      for (int i = 0; i < kPairs / 2; ++i) {
+        c[i] = *reinterpret_cast<const float2*>(t + 2 * i);
+        s[i] = *reinterpret_cast<const float2*>(t + kEntries + 2 * i);
+      }
+    }
+    int b, l;
+    place(at, local, b, l);
+    T* o0 = static_cast<T*>(p.out[0]) + b * p.out_stride[0][0] + l * p.out_stride[0][1] + e0;
+    T* o1 = static_cast<T*>(p.out[1]) + b * p.out_stride[1][0] + l * p.out_stride[1][1] + e0;
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+      const int h = h0 + (at.step * kHeads + u) * p.head_slots;
+      if (h >= p.heads) break;
+      T* o = h < p.heads_q ? o0 + h * p.out_stride[0][2]
+                           : o1 + (h - p.heads_q) * p.out_stride[1][2];
+      const uint4* v = chunks + (st * kRopeChunks + u * kParts) * kRopeThreads;
+      float x[V], y[V];
+      Elem<T>::unpack(v[0], x);
+      if constexpr (kHalves) {
+        float z[V], w[V];
+        Elem<T>::unpack(v[kRopeThreads], z);
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          const float2 xi = make_float2(x[i], x[i + 1]), zi = make_float2(z[i], z[i + 1]);
+          const float2 ns = make_float2(-s[i / 2].x, -s[i / 2].y);
+          const float2 a = __ffma2_rn(xi, c[i / 2], __fmul2_rn(zi, ns));
+          const float2 d = __ffma2_rn(xi, s[i / 2], __fmul2_rn(zi, c[i / 2]));
+          y[i] = a.x, y[i + 1] = a.y;
+          w[i] = d.x, w[i + 1] = d.y;
+        }
+        __stcs(reinterpret_cast<uint4*>(o), Elem<T>::pack(y));
+        __stcs(reinterpret_cast<uint4*>(o + half), Elem<T>::pack(w));
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {  // two pairs at once
+          const float2 xi = make_float2(x[i], x[i + 2]), zi = make_float2(x[i + 1], x[i + 3]);
+          const float2 ns = make_float2(-s[i / 4].x, -s[i / 4].y);
+          const float2 a = __ffma2_rn(xi, c[i / 4], __fmul2_rn(zi, ns));
+          const float2 d = __ffma2_rn(xi, s[i / 4], __fmul2_rn(zi, c[i / 4]));
+          y[i] = a.x, y[i + 2] = a.y;
+          y[i + 1] = d.x, y[i + 3] = d.y;
+        }
+        __stcs(reinterpret_cast<uint4*>(o), Elem<T>::pack(y));
+      }
+    }
+  };
+  // In place, a thread reads only chunks that it writes itself, later: copying ahead is safe.
+  At cur, pre;
+  pre.base = blockIdx.x * (uint32_t)p.tokens;
+  pre.b = (int)(pre.base / (uint32_t)p.len);
+  pre.l = (int)(pre.base % (uint32_t)p.len);
+  pre.step = 0;
+  cur = pre;
+#pragma unroll
+  for (int i = 0; i + 1 < kStages; ++i) {
+    load(pre, i);
+    next(pre);
+  }
+  cp_async_wait<kStages - 2>();
+  int which = 0, st = 0;
+  fill(cur, 0, which);
   __syncthreads();
-  while (at0.base < rows) {
-    const At at1 = next(at0);
-    load(b, at1.base, at1.b, at1.l, at1.step);
-    turn(a, at0.base, at0.step, which);
-    if (at1.base >= rows) break;
-    if (at1.step == 0) fill(b, which ^= 1);
-    __syncthreads();
-    at0 = next(at1);
-    load(a, at0.base, at0.b, at0.l, at0.step);
-    turn(b, at1.base, at1.step, which);
-    if (at0.base >= rows) break;
-    if (at0.step == 0) fill(a, which ^= 1);
+  while (cur.base < rows) {  // the same in the whole CTA
+    load(pre, st == 0 ? kStages - 1 : st - 1);  // the stage of the step before this one
+    next(pre);
+    cp_async_wait<kStages - 2>();  // this step and the next one have arrived
+    turn(cur, st, which);
+    next(cur);
+    if (++st == kStages) st = 0;
+    if (cur.step == 0 && cur.base < rows) fill(cur, st, which ^= 1);
     __syncthreads();
   }
+  cp_async_wait<0>();
 }
 
 }  // namespace ltx
