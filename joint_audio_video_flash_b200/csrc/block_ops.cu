@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "host_common.h"
 #include "layer_norm.cuh"
@@ -78,160 +79,218 @@ int launch_rope(ltx::RopeParams& p, bool halves, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- layer norm
-// CTAs per group that fill the device once, and no more than there are row slots to take.
-int norm_ctas(int resident, long long groups, long long rows_per_group, int slots) {
-  const long long want = (rows_per_group + slots - 1) / slots;
-  return (int)std::max<long long>(1, std::min<long long>(want, resident / groups));
-}
-
-// Warps per row for `per_lane` elements a lane at most; 0 when a row does not fit a CTA.
-int norm_warps(int cols, int per_lane) {
-  for (int wpr = 1; wpr <= ltx::kNormWarps; wpr *= 2)
-    if ((long long)wpr * 32 * per_lane >= cols) return wpr;
+// Threads per row for at most `per_lane` elements a thread, `cols` of them behind up to
+// `shift` of the row before; 0 when a row does not fit a CTA.
+int norm_lanes(int cols, int shift, int per_lane) {
+  for (int lanes = ltx::kNormMinLanes; lanes <= ltx::kNormThreads; lanes *= 2)
+    if ((long long)lanes * per_lane >= (long long)cols + shift) return lanes;
   return 0;
 }
 
-// Every row and the weights start on 16 bytes and hold whole 16-byte chunks.
-bool norm_vector(const ltx::NormParams& p, int item, bool grad) {
-  uintptr_t at = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.out) |
-                 reinterpret_cast<uintptr_t>(p.weight) | reinterpret_cast<uintptr_t>(p.bias);
-  long long strides = (p.x_stride | p.out_stride | p.cols) * item;
-  if (grad) {
-    at |= reinterpret_cast<uintptr_t>(p.dy);
-    strides |= p.dy_stride * item;
-  }
-  return ((at | (uintptr_t)strides) & 15u) == 0;
+// CTAs per group that fill the device once, and no more than there are row slots to take;
+// whole multiples of what keeps every slot to rows of one shift.
+int norm_ctas(int resident, long long groups, long long rows_per_group, int lanes, int phases) {
+  const int slots = ltx::kNormThreads / lanes;
+  const int multiple = std::max(1, phases / slots);  // both are powers of two
+  const long long want = (rows_per_group + slots - 1) / slots;
+  const long long fit = std::min<long long>(want, resident / groups);
+  return (int)std::max<long long>(1, fit / multiple) * multiple;
 }
 
-template <typename T, int V, int kChunks>
-int launch_norm(ltx::NormParams& p, long long groups, int wpr, cudaStream_t stream) {
-  const int resident = ltx::resident_ctas<ltx::ltx_layer_norm<T, V, kChunks>>(ltx::kNormThreads);
+// How the rows of a call lie against 16-byte boundaries.
+struct NormLayout {
+  bool vector;  // x, dy and out agree, so 16-byte chunks of them correspond
+  bool edge;    // a row may start or end inside a chunk
+  int phases;   // rows until the same alignment returns
+};
+
+NormLayout norm_layout(const ltx::NormParams& p, long long rows, int item, bool grad) {
+  auto of = [&](const void* base, long long stride) {
+    return std::pair<uintptr_t, uintptr_t>(reinterpret_cast<uintptr_t>(base) & 15u,
+                                           rows > 1 ? (uintptr_t)(stride * item) & 15u : 0);
+  };
+  const auto x = of(p.x, p.x_stride);
+  NormLayout l;
+  l.vector = of(p.out, p.out_stride) == x && (!grad || of(p.dy, p.dy_stride) == x);
+  const uintptr_t vectors =
+      (reinterpret_cast<uintptr_t>(p.weight) | reinterpret_cast<uintptr_t>(p.bias)) & 15u;
+  l.edge = x.first || x.second || vectors || ((long long)p.cols * item) % 16 != 0;
+  l.phases = 1;
+  while ((x.second * l.phases) % 16 != 0) l.phases *= 2;
+  return l;
+}
+
+using ltx::NormFit;
+
+NormFit norm_fit(bool edge, int cols, int lanes, int per_lane) {
+  return edge ? ltx::kNormEdge : cols == lanes * per_lane ? ltx::kNormFull : ltx::kNormWhole;
+}
+
+template <typename T, int kChunks, NormFit kFit>
+int launch_norm(ltx::NormParams& p, long long groups, int lanes, int phases,
+                cudaStream_t stream) {
+  using L = ltx::NormShape<kChunks, kFit>;
+  const int resident =
+      ltx::resident_ctas<ltx::ltx_layer_norm<T, kChunks, kFit>>(ltx::kNormThreads, L::kSmem);
   if (resident < 1) return LTXATTN_ERR_CUDA;
-  p.wpr = wpr;
-  p.ctas_per_group = norm_ctas(resident, groups, p.rows_per_group, ltx::kNormWarps / wpr);
-  ltx::ltx_layer_norm<T, V, kChunks>
-      <<<(unsigned)(groups * p.ctas_per_group), ltx::kNormThreads, 0, stream>>>(p);
+  p.lanes = lanes;
+  p.phases = phases;
+  p.ctas_per_group = norm_ctas(resident, groups, p.rows_per_group, lanes, phases);
+  ltx::ltx_layer_norm<T, kChunks, kFit>
+      <<<(unsigned)(groups * p.ctas_per_group), ltx::kNormThreads, L::kSmem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
+}
+
+template <typename T, int kChunks>
+int launch_norm_fit(ltx::NormParams& p, long long groups, int lanes, const NormLayout& l,
+                    cudaStream_t stream) {
+  switch (norm_fit(l.edge, p.cols, lanes, kChunks * ltx::Elem<T>::kVec)) {
+    case ltx::kNormFull:
+      return launch_norm<T, kChunks, ltx::kNormFull>(p, groups, lanes, 1, stream);
+    case ltx::kNormWhole:
+      return launch_norm<T, kChunks, ltx::kNormWhole>(p, groups, lanes, 1, stream);
+    default:
+      return launch_norm<T, kChunks, ltx::kNormEdge>(p, groups, lanes, l.phases, stream);
+  }
 }
 
 template <typename T>
 int layer_norm_forward(ltx::NormParams& p, long long groups, cudaStream_t stream) {
   constexpr int V = ltx::Elem<T>::kVec;
-  if (norm_vector(p, (int)sizeof(T), false)) {
-    if (int w = norm_warps(p.cols, 4 * V)) return launch_norm<T, V, 4>(p, groups, w, stream);
-    if (int w = norm_warps(p.cols, 8 * V)) return launch_norm<T, V, 8>(p, groups, w, stream);
-  } else {
-    if (int w = norm_warps(p.cols, 8)) return launch_norm<T, 1, 8>(p, groups, w, stream);
-    if (int w = norm_warps(p.cols, 16)) return launch_norm<T, 1, 16>(p, groups, w, stream);
+  const NormLayout l = norm_layout(p, groups * p.rows_per_group, (int)sizeof(T), false);
+  const int shift = l.edge ? V - 1 : 0;
+  if (l.vector) {
+    if (int n = norm_lanes(p.cols, shift, 4 * V))
+      return launch_norm_fit<T, 4>(p, groups, n, l, stream);
+    if (int n = norm_lanes(p.cols, shift, 8 * V))
+      return launch_norm_fit<T, 8>(p, groups, n, l, stream);
   }
   const int resident = ltx::resident_ctas<ltx::ltx_layer_norm_wide<T>>(ltx::kNormThreads);
   if (resident < 1) return LTXATTN_ERR_CUDA;
-  p.wpr = ltx::kNormWarps;
-  p.ctas_per_group = norm_ctas(resident, groups, p.rows_per_group, 1);
+  p.lanes = ltx::kNormThreads;
+  p.phases = 1;
+  p.ctas_per_group = norm_ctas(resident, groups, p.rows_per_group, p.lanes, 1);
   ltx::ltx_layer_norm_wide<T>
       <<<(unsigned)(groups * p.ctas_per_group), ltx::kNormThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
 }
 
-// The plan of a backward call, the same for the workspace query and the launch.
-enum class GradKernel { kVector2, kVector4, kScalar8, kScalar16, kWide };
+// The plan of a backward call.
 struct GradPlan {
-  GradKernel kernel;
-  int wpr, ctas_per_group;
+  int chunks;  // 2 or 4 a thread; 0: rows too wide, or no common alignment
+  NormFit fit;
+  int lanes, phases, ctas_per_group;
   size_t workspace;  // bytes of partials
 };
 
-template <typename T, int V, int kChunks>
+template <typename T, int kChunks, NormFit kFit>
 int grad_resident(bool affine) {
-  return affine ? ltx::resident_ctas<ltx::ltx_layer_norm_grad<T, V, kChunks, true>>(
-                      ltx::kNormThreads)
-                : ltx::resident_ctas<ltx::ltx_layer_norm_grad<T, V, kChunks, false>>(
-                      ltx::kNormThreads);
+  constexpr int kSmem = ltx::NormGradShape<kChunks>::kSmem, n = ltx::kNormThreads;
+  return affine ? ltx::resident_ctas<ltx::ltx_layer_norm_grad<T, kChunks, kFit, true>>(n, kSmem)
+                : ltx::resident_ctas<ltx::ltx_layer_norm_grad<T, kChunks, kFit, false>>(n, kSmem);
+}
+
+template <typename T, int kChunks>
+int grad_resident(NormFit fit, bool affine) {
+  return fit == ltx::kNormFull    ? grad_resident<T, kChunks, ltx::kNormFull>(affine)
+         : fit == ltx::kNormWhole ? grad_resident<T, kChunks, ltx::kNormWhole>(affine)
+                                  : grad_resident<T, kChunks, ltx::kNormEdge>(affine);
 }
 
 template <typename T>
-int grad_plan(int cols, bool vector, bool affine, long long groups, long long rows_per_group,
-              GradPlan* plan) {
+int grad_plan(int cols, const NormLayout& l, bool affine, long long groups,
+              long long rows_per_group, GradPlan* plan) {
   constexpr int V = ltx::Elem<T>::kVec;
+  const int shift = l.edge ? V - 1 : 0;
   int resident = 0;
-  if (vector && (plan->wpr = norm_warps(cols, 2 * V))) {
-    plan->kernel = GradKernel::kVector2;
-    resident = grad_resident<T, V, 2>(affine);
-  } else if (vector && (plan->wpr = norm_warps(cols, 4 * V))) {
-    plan->kernel = GradKernel::kVector4;
-    resident = grad_resident<T, V, 4>(affine);
-  } else if (!vector && (plan->wpr = norm_warps(cols, 8))) {
-    plan->kernel = GradKernel::kScalar8;
-    resident = grad_resident<T, 1, 8>(affine);
-  } else if (!vector && (plan->wpr = norm_warps(cols, 16))) {
-    plan->kernel = GradKernel::kScalar16;
-    resident = grad_resident<T, 1, 16>(affine);
-  } else {
-    plan->kernel = GradKernel::kWide;
-    plan->wpr = ltx::kNormWarps;
+  plan->fit = ltx::kNormEdge;
+  plan->lanes = 0;
+  plan->phases = l.edge ? l.phases : 1;
+  // a row's fixed costs (sums, barrier, addresses) fall on fewer elements with 2 chunks a
+  // thread, but twice the warps fit: 4 are faster where rows of 2-byte elements come in whole
+  // chunks (30720 x 4096 bf16: 135 us against 158), 2 otherwise (20000 x 1537 bf16: 103 us
+  // against 134; 4-byte elements are bound by memory either way)
+  const int first = sizeof(T) == 2 && !l.edge ? 4 : 2;
+  for (int chunks : {first, 6 - first}) {
+    if (!l.vector || !(plan->lanes = norm_lanes(cols, shift, chunks * V))) continue;
+    plan->chunks = chunks;
+    plan->fit = norm_fit(l.edge, cols, plan->lanes, chunks * V);
+    resident = chunks == 2 ? grad_resident<T, 2>(plan->fit, affine)
+                           : grad_resident<T, 4>(plan->fit, affine);
+    break;
+  }
+  if (!plan->lanes || !l.vector) {
+    plan->chunks = 0;
+    plan->lanes = ltx::kNormThreads;
+    plan->phases = 1;
     resident = ltx::resident_ctas<ltx::ltx_layer_norm_grad_wide<T>>(ltx::kNormThreads);
   }
   if (resident < 1) return LTXATTN_ERR_CUDA;
-  plan->ctas_per_group =
-      norm_ctas(resident, groups, rows_per_group, ltx::kNormWarps / plan->wpr);
+  plan->ctas_per_group = norm_ctas(resident, groups, rows_per_group, plan->lanes, plan->phases);
   plan->workspace = affine && plan->ctas_per_group > 1
                         ? (size_t)groups * plan->ctas_per_group * 2 * cols * sizeof(float)
                         : 0;
   return LTXATTN_OK;
 }
 
-int grad_plan_of(int dtype, int cols, bool vector, bool affine, long long groups,
+int grad_plan_of(int dtype, int cols, const NormLayout& l, bool affine, long long groups,
                  long long rows_per_group, GradPlan* plan) {
   switch (dtype) {
     case LTXATTN_BF16:
-      return grad_plan<__nv_bfloat16>(cols, vector, affine, groups, rows_per_group, plan);
+      return grad_plan<__nv_bfloat16>(cols, l, affine, groups, rows_per_group, plan);
     case LTXATTN_FP16:
-      return grad_plan<__half>(cols, vector, affine, groups, rows_per_group, plan);
-    default:
-      return grad_plan<float>(cols, vector, affine, groups, rows_per_group, plan);
+      return grad_plan<__half>(cols, l, affine, groups, rows_per_group, plan);
+    default: return grad_plan<float>(cols, l, affine, groups, rows_per_group, plan);
   }
 }
 
-template <typename T, int V, int kChunks>
+template <typename T, int kChunks, NormFit kFit>
 cudaError_t launch_grad(const ltx::NormParams& p, long long groups, bool affine,
                         cudaStream_t stream) {
+  constexpr int kSmem = ltx::NormGradShape<kChunks>::kSmem;
   const unsigned grid = (unsigned)(groups * p.ctas_per_group);
-  // several row slots (cols <= 4 warps' worth, 32 KB at most) meet in shared memory
-  const size_t smem = affine && p.wpr < ltx::kNormWarps ? 2 * p.cols * sizeof(float) : 0;
   if (affine)
-    ltx::ltx_layer_norm_grad<T, V, kChunks, true><<<grid, ltx::kNormThreads, smem, stream>>>(p);
+    ltx::ltx_layer_norm_grad<T, kChunks, kFit, true>
+        <<<grid, ltx::kNormThreads, kSmem, stream>>>(p);
   else
-    ltx::ltx_layer_norm_grad<T, V, kChunks, false><<<grid, ltx::kNormThreads, 0, stream>>>(p);
+    ltx::ltx_layer_norm_grad<T, kChunks, kFit, false>
+        <<<grid, ltx::kNormThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <typename T, int kChunks>
+cudaError_t launch_grad(NormFit fit, const ltx::NormParams& p, long long groups, bool affine,
+                        cudaStream_t stream) {
+  return fit == ltx::kNormFull ? launch_grad<T, kChunks, ltx::kNormFull>(p, groups, affine, stream)
+         : fit == ltx::kNormWhole
+             ? launch_grad<T, kChunks, ltx::kNormWhole>(p, groups, affine, stream)
+             : launch_grad<T, kChunks, ltx::kNormEdge>(p, groups, affine, stream);
 }
 
 template <typename T>
 int layer_norm_grad(const ltx::NormParams& p, long long groups, bool affine,
                     const GradPlan& plan, cudaStream_t stream) {
-  constexpr int V = ltx::Elem<T>::kVec;
   cudaError_t e = cudaSuccess;
-  switch (plan.kernel) {
-    case GradKernel::kVector2: e = launch_grad<T, V, 2>(p, groups, affine, stream); break;
-    case GradKernel::kVector4: e = launch_grad<T, V, 4>(p, groups, affine, stream); break;
-    case GradKernel::kScalar8: e = launch_grad<T, 1, 8>(p, groups, affine, stream); break;
-    case GradKernel::kScalar16: e = launch_grad<T, 1, 16>(p, groups, affine, stream); break;
-    case GradKernel::kWide: {
-      const unsigned grid = (unsigned)(groups * p.ctas_per_group);
-      if (affine) {  // ahead of dx, which may replace x or dy
-        const unsigned blocks = (unsigned)std::min(64, (p.cols + ltx::kNormThreads - 1) /
-                                                           ltx::kNormThreads);
-        ltx::ltx_layer_norm_grad_cols<T><<<dim3(grid, blocks), ltx::kNormThreads, 0, stream>>>(p);
-        e = cudaGetLastError();
-      }
-      if (e == cudaSuccess) {
-        ltx::ltx_layer_norm_grad_wide<T><<<grid, ltx::kNormThreads, 0, stream>>>(p);
-        e = cudaGetLastError();
-      }
+  if (plan.chunks == 2) {
+    e = launch_grad<T, 2>(plan.fit, p, groups, affine, stream);
+  } else if (plan.chunks == 4) {
+    e = launch_grad<T, 4>(plan.fit, p, groups, affine, stream);
+  } else {
+    const unsigned grid = (unsigned)(groups * p.ctas_per_group);
+    if (affine) {  // ahead of dx, which may replace x or dy
+      const unsigned blocks =
+          (unsigned)std::min(64, (p.cols + ltx::kNormThreads - 1) / ltx::kNormThreads);
+      ltx::ltx_layer_norm_grad_cols<T><<<dim3(grid, blocks), ltx::kNormThreads, 0, stream>>>(p);
+      e = cudaGetLastError();
+    }
+    if (e == cudaSuccess) {
+      ltx::ltx_layer_norm_grad_wide<T><<<grid, ltx::kNormThreads, 0, stream>>>(p);
+      e = cudaGetLastError();
     }
   }
   if (e == cudaSuccess && p.partial) {
     const int col_blocks = (2 * p.cols + 31) / 32;
-    ltx::ltx_layer_norm_grad_sum<<<(unsigned)(groups * col_blocks), ltx::kNormThreads, 0,
+    ltx::ltx_layer_norm_grad_sum<<<(unsigned)(groups * col_blocks), ltx::kNormSumWarps * 32, 0,
                                    stream>>>(p.partial, p.dweight, p.dbias, p.ctas_per_group,
                                              p.cols, col_blocks);
     e = cudaGetLastError();
@@ -423,13 +482,18 @@ int ltxattn_layer_norm_workspace(long long rows, int cols, long long groups, int
   if (!bytes) return LTXATTN_ERR_INVALID_ARG;
   int st = norm_sizes(rows, cols, groups, dtype);
   if (st != LTXATTN_OK) return st;
-  // addresses decide between the two register kernels: the larger of their needs
+  // addresses decide which kernel runs: the largest of their needs
   unsigned long long most = 0;
-  for (bool vector : {false, true}) {
-    GradPlan plan;
-    st = grad_plan_of(dtype, cols, vector, true, groups, rows / groups, &plan);
-    if (st != LTXATTN_OK) return st;
-    most = std::max<unsigned long long>(most, plan.workspace);
+  const int item = elem_size(dtype);
+  const bool whole = ((long long)cols * item) % 16 == 0;
+  for (int i = whole ? 0 : 1; i < 3; ++i) {
+    for (int phases = 1; phases <= (i == 1 ? 16 / item : 1); phases *= 2) {
+      const NormLayout l{i < 2, i == 1, phases};
+      GradPlan plan;
+      st = grad_plan_of(dtype, cols, l, true, groups, rows / groups, &plan);
+      if (st != LTXATTN_OK) return st;
+      most = std::max<unsigned long long>(most, plan.workspace);
+    }
   }
   *bytes = most;
   return LTXATTN_OK;
@@ -501,13 +565,15 @@ int ltxattn_layer_norm_backward(const void* dy, const void* x, const void* weigh
   p.dweight = dweight;
   p.dbias = dbias;
   GradPlan plan;
-  st = grad_plan_of(dtype, cols, norm_vector(p, item, true), affine, groups, rows / groups, &plan);
+  st = grad_plan_of(dtype, cols, norm_layout(p, rows, item, true), affine, groups, rows / groups,
+                    &plan);
   if (st != LTXATTN_OK) return st;
   if (plan.workspace > 0) {
     if (!workspace || workspace_bytes < plan.workspace) return LTXATTN_ERR_INVALID_ARG;
     p.partial = static_cast<float*>(workspace);
   }
-  p.wpr = plan.wpr;
+  p.lanes = plan.lanes;
+  p.phases = plan.phases;
   p.ctas_per_group = plan.ctas_per_group;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   switch (dtype) {
