@@ -47,7 +47,12 @@ namespace ltx {
 
 struct MaskedBwdParams {
   MaskedShape s;
-  float2* stat;        // [batch][heads][q_len]: lse (+inf for a query that sees no key), delta
+  const __nv_bfloat16* out;  // dQ only, with d_out and lse: delta
+  const __nv_bfloat16* d_out;
+  const float* lse;
+  long long out_stride[3], d_out_stride[3];
+  float2* stat;        // [batch][heads][q_len]: lse (+inf for a query that sees no key), delta;
+                       // written by the dQ kernel, read by the dK and dV kernel
   float scale;
   int parts;           // parts of the walk, each with an fp32 partial
   __nv_bfloat16* d0;   // dQ, or dK
@@ -57,41 +62,6 @@ struct MaskedBwdParams {
   float* part1;        // dV; sum P b K (dQ with a cap)
   float* part_e;       // [parts][batch][heads][len]: e (dQ)
 };
-
-constexpr int kStatTokens = 64;  // tokens per CTA of ltx_masked_stat
-
-// stat = (lse or +inf, delta); one half-warp (D = 128) or quarter (64) per row.
-template <int D>
-__global__ void __launch_bounds__(256)
-    ltx_masked_stat(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ d_out,
-                    const float* __restrict__ lse, float2* __restrict__ stat, int heads, int q_len,
-                    long long ob, long long ol, long long oh, long long db, long long dl,
-                    long long dh) {
-  constexpr int kLanes = D / 8;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x % kLanes;
-  for (int t = threadIdx.x / kLanes; t < kStatTokens; t += 256 / kLanes) {
-    const int i = blockIdx.x * kStatTokens + t;
-    float sum = 0.0f;
-    if (i < q_len) {
-      const uint4 o = __ldg(reinterpret_cast<const uint4*>(out + b * ob + i * ol + h * oh) + lane);
-      const uint4 d = __ldg(reinterpret_cast<const uint4*>(d_out + b * db + i * dl + h * dh) + lane);
-      const uint32_t ou[4] = {o.x, o.y, o.z, o.w}, du[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        sum = fmaf(__uint_as_float(ou[x] << 16), __uint_as_float(du[x] << 16), sum);
-        sum = fmaf(__uint_as_float(ou[x] & 0xffff0000u), __uint_as_float(du[x] & 0xffff0000u), sum);
-      }
-    }
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0 && i < q_len) {
-      const size_t at = ((size_t)b * heads + h) * q_len + i;
-      const float l = __ldg(lse + at);
-      stat[at] = make_float2(l == -INFINITY ? INFINITY : l, sum);
-    }
-  }
-}
 
 // 1 - tanh^2 of a capped score (log2 units).
 __device__ __forceinline__ float cap_bend(float capped, float inv_cap_log2) {
@@ -235,6 +205,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
   const MaskedPlace at_work = masked_place(p.s.kv_heads, p.s.batch, p.parts);
   const int hk = at_work.head, b = at_work.b, part = at_work.part;
 
+  grid_dependency_wait();
   if (warp == 2) {
     const MaskedDoc m = masked_find<true>(p.s, b, at_work.unit, kBlockN);
     if (lane == 0) *shared_doc = m;
@@ -259,6 +230,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     *abort_flag = (*reinterpret_cast<volatile int*>(p.s.status) != kDevOk) ? 1 : 0;
     fence_mbar_init();
   }
+  grid_dependents_launch();
   __syncthreads();
   const MaskedDoc m = *shared_doc;
   if (m.tile < 0) return;
@@ -498,7 +470,8 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         masked_scores<true, false>(s, p.s, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int x = 0; x < 64; ++x) bent[x] = cap_bend(s[x], inv_cap);
-        if constexpr (kBias) masked_bias<true>(s, p.s, slope, (float)(i0 + (m.nk - m.nq) - j), 1.0f);
+        if constexpr (kBias)
+          masked_bias<true>(s, p.s, slope, (float)(i0 + (m.nk - m.nq) - j), 1.0f);
       } else if constexpr (kBias) {
         masked_bias<false>(s, p.s, slope, (float)(i0 + (m.nk - m.nq) - j), 1.0f);
       }
@@ -597,8 +570,8 @@ struct BwdQSmem {
   static constexpr int kDo = kQ + kTileBytes;
   static constexpr int kK = kDo + kTileBytes;
   static constexpr int kV = kK + kKStages * kTileBytes;
-  static constexpr int kSum = kV + kVStages * kTileBytes;  // [128] fp32: e of group 1
-  static constexpr int kBar = kSum + 128 * 4;
+  static constexpr int kSum = kV + kVStages * kTileBytes;  // [2][128] fp32: delta, then e
+  static constexpr int kBar = kSum + 2 * 128 * 4;
   static constexpr int bQF = 0;
   static constexpr int bOF = 1;
   static constexpr int bKF = 2;
@@ -676,6 +649,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     *abort_flag = (*reinterpret_cast<volatile int*>(p.s.status) != kDevOk) ? 1 : 0;
     fence_mbar_init();
   }
+  grid_dependents_launch();
   __syncthreads();
   const MaskedDoc m = *shared_doc;
   if (m.tile < 0) return;
@@ -840,9 +814,37 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     const int row = wq * 32 + lane;
     const int i = i0 + row;
     const uint32_t trow = tmem + ((uint32_t)(wq * 32) << 16);
+    // delta: half of the channels each, while the first tiles are on their way
+    float* sums = reinterpret_cast<float*>(smem + L::kSum);
     float2 st = make_float2(INFINITY, 0.0f);  // behind the last query: P = 0
     const size_t stat_at = ((size_t)b * p.s.heads + h) * p.s.q_len + m.q0 + i;
-    if (i < m.nq) st = p.stat[stat_at];
+    {
+      float dot = 0.0f;
+      if (i < m.nq) {
+        const long long tok = m.q0 + i;
+        const uint4* o = reinterpret_cast<const uint4*>(
+            p.out + b * p.out_stride[0] + tok * p.out_stride[1] + h * p.out_stride[2] + g * (D / 2));
+        const uint4* d = reinterpret_cast<const uint4*>(p.d_out + b * p.d_out_stride[0] +
+                                                        tok * p.d_out_stride[1] +
+                                                        h * p.d_out_stride[2] + g * (D / 2));
+        const float l = __ldg(p.lse + stat_at);
+        st.x = l == -INFINITY ? INFINITY : l;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint4 ov = __ldg(o + x), dv = __ldg(d + x);
+          const uint32_t ou[4] = {ov.x, ov.y, ov.z, ov.w}, du[4] = {dv.x, dv.y, dv.z, dv.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            dot = fmaf(__uint_as_float(ou[y] << 16), __uint_as_float(du[y] << 16), dot);
+            dot = fmaf(__uint_as_float(ou[y] & 0xffff0000u), __uint_as_float(du[y] & 0xffff0000u),
+                       dot);
+          }
+        }
+      }
+      sums[g * kBlockM + row] = dot;
+      named_bar_sync(2, 256);  // ahead of every wait that may fail
+      if (i < m.nq) st.y = sums[row] + sums[kBlockM + row];
+    }
     const int lim = masked_limit(m, p.s.causal, i);
     const int lim_warp = masked_limit(m, p.s.causal, i0 + wq * 32);
     float slope = 0.0f;
@@ -920,8 +922,8 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       if (lane == 0) mbar_arrive(bar(L::bDs + g));
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::bEnd), 0, ctl));
-    float* sums = reinterpret_cast<float*>(smem + L::kSum);
     float e = off2.x + off2.y;
+    named_bar_sync(2, 256);  // both groups have read delta (every wait above is bounded)
     if (g == 1) sums[row] = e;
     ok = named_bar_and(1, 256, ok && !*abort_flag);
     if (ok) {
@@ -933,7 +935,10 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       if (p.parts > 1) {
         // the parts' sums meet in ltx_masked_bwd_sum
         if (g == 0) {
-          if (i < m.nq) p.part_e[rows0 + i] = e;
+          if (i < m.nq) {
+            p.part_e[rows0 + i] = e;
+            if (part == 0) p.stat[stat_at] = st;
+          }
           masked_store<D>(trow + L::kColQ, n > 0, p.scale, smem + L::kQ, i0, m.nq, out,
                           p.stride0[1], p.part0 + rows0 * D);
         } else if (kFix) {
@@ -941,7 +946,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
                           p.stride0[1], p.part1 + rows0 * D);
         }
       } else if (g == 0) {
-        if (i < m.nq) p.stat[stat_at].y = st.y + e;
+        if (i < m.nq) p.stat[stat_at] = make_float2(st.x, st.y + e);
         masked_store<D>(trow + L::kColQ, n > 0, p.scale, smem + L::kQ, i0, m.nq, out,
                         p.stride0[1], nullptr, kFix ? trow + L::kColPk : 0u, e);
       }
@@ -957,50 +962,58 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
   }
 }
 
-// Sum of the fp32 partials of one gradient, in a fixed order, rounded to bf16.  One thread per
-// 4 channels; rows of no document are left as they are.  part_e (dQ): the parts' e, whose sum
-// goes into stat, and with part_fix takes that many times the sum of its partials off.
-template <int D>
+// Sum of the fp32 partials of gradients of one shape, in a fixed order, rounded to bf16.  One
+// thread per 4 channels; rows of no document are left as they are.
+//   kDq   part0: dQ's, part1: sum P b K's (or null), part_e: e's: e goes into stat, and e times
+//         the sum of part1 is taken off
+//   else  part0: dK's, part1: dV's, the second half of the grid
+template <int D, bool kDq>
 __global__ void __launch_bounds__(kCombineThreads)
-    ltx_masked_bwd_sum(const float* __restrict__ part, const float* __restrict__ part_fix,
-                       const float* __restrict__ part_e, float2* __restrict__ stat,
-                       __nv_bfloat16* __restrict__ out, int parts, int batch, int heads, int len,
-                       const int* __restrict__ starts, int docs, long long sb, long long sl,
-                       long long sh) {
+    ltx_masked_bwd_sum(const __grid_constant__ MaskedBwdParams p) {
+  grid_dependency_wait();
+  grid_dependents_launch();
   constexpr int kVec = D / 4;
+  const int heads = kDq ? p.s.heads : p.s.kv_heads, len = kDq ? p.s.q_len : p.s.kv_len;
+  const int docs = p.s.docs;
+  const long long rows = (long long)p.s.batch * heads * len;
   const long long tid = (long long)blockIdx.x * kCombineThreads + threadIdx.x;
-  const long long rows = (long long)batch * heads * len;
-  const long long row = tid / kVec;
+  long long row = tid / kVec;
+  const bool second = !kDq && row >= rows;
+  if (second) row -= rows;
   if (row >= rows) return;
   const int c = (int)(tid % kVec), i = (int)(row % len);
   const int h = (int)(row / len % heads), b = (int)(row / len / heads);
   if (docs) {
-    const int* s = starts + (size_t)b * (docs + 1);
+    const int* s = (kDq ? p.s.q_starts : p.s.kv_starts) + (size_t)b * (docs + 1);
     if (i < __ldg(s) || i >= __ldg(s + docs)) return;
   }
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int x = 0; x < parts; ++x) {
-    const float4 v = reinterpret_cast<const float4*>(part + (x * rows + row) * D)[c];
-    a.x += v.x;
-    a.y += v.y;
-    a.z += v.z;
-    a.w += v.w;
-  }
-  if (part_e) {
-    float e = 0.0f;
-    for (int x = 0; x < parts; ++x) e += part_e[x * rows + row];
-    if (part_fix) {
-      for (int x = 0; x < parts; ++x) {
-        const float4 v = reinterpret_cast<const float4*>(part_fix + (x * rows + row) * D)[c];
-        a.x = fmaf(-e, v.x, a.x);
-        a.y = fmaf(-e, v.y, a.y);
-        a.z = fmaf(-e, v.z, a.z);
-        a.w = fmaf(-e, v.w, a.w);
-      }
+  auto total = [&](const float* part) {
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int x = 0; x < p.parts; ++x) {
+      const float4 v = reinterpret_cast<const float4*>(part + (x * rows + row) * D)[c];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
     }
-    if (c == 0) stat[row].y += e;
+    return a;
+  };
+  float4 a = total(second ? p.part1 : p.part0);
+  if constexpr (kDq) {
+    float e = 0.0f;
+    for (int x = 0; x < p.parts; ++x) e += p.part_e[x * rows + row];
+    if (p.part1) {
+      const float4 f = total(p.part1);
+      a.x = fmaf(-e, f.x, a.x);
+      a.y = fmaf(-e, f.y, a.y);
+      a.z = fmaf(-e, f.z, a.z);
+      a.w = fmaf(-e, f.w, a.w);
+    }
+    if (c == 0) p.stat[row].y += e;
   }
-  *reinterpret_cast<uint2*>(out + b * sb + i * sl + h * sh + c * 4) =
+  const long long* st = second ? p.stride1 : p.stride0;
+  *reinterpret_cast<uint2*>((second ? p.d1 : p.d0) + b * st[0] + i * st[1] + h * st[2] + c * 4) =
       make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
 }
 

@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     *abort_flag = (*reinterpret_cast<volatile int*>(p.s.status) != kDevOk) ? 1 : 0;
     fence_mbar_init();
   }
+  grid_dependents_launch();
   __syncthreads();
   const MaskedDoc m = *shared_doc;
   if (m.tile < 0) return;  // fewer units than the host's bound; nothing was allocated yet
@@ -734,9 +735,12 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 
 // Merge of the key parts: L = max lse_p, w_p = 2^(lse_p - L), out = sum w_p o_p / sum w_p.
 // One thread per 4 channels of a row; rows of no document are left as they are.
+constexpr int kMaskedMergeBatch = 8;  // parts whose loads are in flight together
+
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
     ltx_masked_combine(const __grid_constant__ MaskedFwdParams p) {
+  grid_dependency_wait();
   constexpr int kVec = D / 4;
   const long long tid = (long long)blockIdx.x * kCombineThreads + threadIdx.x;
   const long long rows = (long long)p.s.batch * p.s.heads * p.s.q_len;
@@ -749,19 +753,41 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int* qs = p.s.q_starts + (size_t)b * (p.s.docs + 1);
     if (i < __ldg(qs) || i >= __ldg(qs + p.s.docs)) return;
   }
-  float top = -INFINITY;
-  for (int x = 0; x < p.parts; ++x) top = fmaxf(top, p.lse_part[x * rows + row]);
-  float sum = 0.0f;
+  // a batch of parts at a time, as the softmax runs over keys: L so far, the sums below it
+  float top = -INFINITY, sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int x = 0; x < p.parts; ++x) {
-    const float l = p.lse_part[x * rows + row];
-    const float w = l == -INFINITY ? 0.0f : ex2(l - top);
-    const float4 o = reinterpret_cast<const float4*>(p.o_part + (x * rows + row) * D)[c];
-    sum += w;
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
+  for (int x0 = 0; x0 < p.parts; x0 += kMaskedMergeBatch) {
+    float l[kMaskedMergeBatch];
+    float4 o[kMaskedMergeBatch];
+    float next = top;
+#pragma unroll
+    for (int x = 0; x < kMaskedMergeBatch; ++x) {
+      l[x] = -INFINITY;
+      o[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (x0 + x < p.parts) {
+        l[x] = p.lse_part[(x0 + x) * rows + row];
+        o[x] = reinterpret_cast<const float4*>(p.o_part + ((x0 + x) * rows + row) * D)[c];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kMaskedMergeBatch; ++x) next = fmaxf(next, l[x]);
+    if (next == -INFINITY) continue;  // nothing seen yet
+    const float f = top == -INFINITY ? 0.0f : ex2(top - next);
+    top = next;
+    sum *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+#pragma unroll
+    for (int x = 0; x < kMaskedMergeBatch; ++x) {
+      const float w = ex2(l[x] - top);  // 2^-inf = 0
+      sum += w;
+      acc.x = fmaf(w, o[x].x, acc.x);
+      acc.y = fmaf(w, o[x].y, acc.y);
+      acc.z = fmaf(w, o[x].z, acc.z);
+      acc.w = fmaf(w, o[x].w, acc.w);
+    }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   *reinterpret_cast<uint2*>(p.out + b * p.out_stride[0] + (long long)i * p.out_stride[1] +

@@ -290,10 +290,9 @@ int layer_norm_grad(const ltx::NormParams& p, long long groups, bool affine,
   }
   if (e == cudaSuccess && p.partial) {
     const int col_blocks = (2 * p.cols + 31) / 32;
-    ltx::ltx_layer_norm_grad_sum<<<(unsigned)(groups * col_blocks), ltx::kNormSumWarps * 32, 0,
-                                   stream>>>(p.partial, p.dweight, p.dbias, p.ctas_per_group,
-                                             p.cols, col_blocks);
-    e = cudaGetLastError();
+    e = ltx::launch_dependent(ltx::ltx_layer_norm_grad_sum, (unsigned)(groups * col_blocks),
+                              ltx::kNormSumWarps * 32, 0, stream, (const float*)p.partial,
+                              p.dweight, p.dbias, p.ctas_per_group, p.cols, col_blocks);
   }
   return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
 }

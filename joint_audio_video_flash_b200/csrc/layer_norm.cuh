@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(kNormThreads, NormGradShape<kChunks>::kMinCtas
     }
   }
   cp_async_wait<0>();
+  grid_dependents_launch();
   if constexpr (kAffine) {
     __syncthreads();  // the stages are idle: [2][cols] of them hold the sums on their way
     float* part = reinterpret_cast<float*>(smem);
@@ -481,6 +482,7 @@ __global__ void __launch_bounds__(kNormSumWarps * 32)
     ltx_layer_norm_grad_sum(const float* __restrict__ partial, float* __restrict__ dweight,
                             float* __restrict__ dbias, int ctas_per_group, int cols,
                             int col_blocks) {
+  grid_dependency_wait();
   __shared__ float sums[kNormSumWarps][32];
   const int group = blockIdx.x / col_blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

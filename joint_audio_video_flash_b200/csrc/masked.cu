@@ -191,15 +191,23 @@ struct FwdPlan {
   int parts;   // key parts
 };
 
-// Parts of a walk of `steps` tiles by each of `ctas` CTAs, as plan_splits in ltxattn.cu counts
-// them: waves of CTAs x (steps a part + `fixed` for the pipeline's fill and the write-out).
-int plan_parts(long long ctas, long long steps, int num_sms, int fixed) {
+// Most units of `rows` rows that `docs` documents (0: one) of `len` rows in all can have: a
+// document of n rows has (n + rows - 1) / rows at most.
+int max_units(int len, int docs, int rows) {
+  return (int)((len + (long long)std::max(docs, 1) * (rows - 1)) / rows);
+}
+
+// Parts of a walk of `steps` tiles by each of `ctas` CTAs, counted in steps: waves of CTAs x
+// (steps a part + kFixed for the pipeline's fill and the write-out), and kMerge for the kernel
+// that adds the parts up.
+int plan_parts(long long ctas, long long steps, int num_sms) {
+  constexpr int kFixed = 4, kMerge = 1;
   if (steps < 4 || ctas >= num_sms) return 1;
   int parts = 1;
   long long best = -1;
   for (int x = 1; x <= (int)std::min<long long>(steps, 64); ++x) {
     const long long waves = (ctas * x + num_sms - 1) / num_sms;
-    const long long cost = waves * ((steps + x - 1) / x + fixed);
+    const long long cost = waves * ((steps + x - 1) / x + kFixed) + (x > 1 ? kMerge : 0);
     if (best < 0 || cost < best) {
       best = cost;
       parts = x;
@@ -215,12 +223,12 @@ FwdPlan plan_forward(const ltx::MaskedShape& s, int num_sms) {
   const long long docs = std::max(s.docs, 1);
   f.alt = (long long)s.q_len * s.pack <= docs * ltx::kBlockM;
   const int rows = ltx::kBlockM / s.pack * (f.alt ? 1 : 2);
-  f.units = (s.q_len + rows - 1) / rows + s.docs;
+  f.units = max_units(s.q_len, s.docs, rows);
   // units that hold rows, as far as the host can tell
   const long long filled = std::max<long long>((s.q_len + rows - 1) / rows, s.docs);
   const long long ctas = filled * (s.heads / s.pack) * s.batch;
   const long long tiles = (s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN;
-  f.parts = plan_parts(ctas, tiles, num_sms, 4);
+  f.parts = plan_parts(ctas, tiles, num_sms);
   return f;
 }
 
@@ -257,10 +265,9 @@ cudaError_t launch_forward(const FwdPlan& f, bool cap, bool bias, const CUtensor
                       : launch_fwd_scores<D, false>(cap, bias, tq, tk, tv, p, f.units, stream);
   if (e == cudaSuccess && p.parts > 1) {
     const long long n = (long long)p.s.batch * p.s.heads * p.s.q_len * (D / 4);
-    ltx::ltx_masked_combine<D>
-        <<<(unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads),
-           ltx::kCombineThreads, 0, stream>>>(p);
-    e = cudaGetLastError();
+    e = ltx::launch_dependent(ltx::ltx_masked_combine<D>,
+                              (unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads),
+                              ltx::kCombineThreads, 0, stream, p);
   }
   return e;
 }
@@ -278,14 +285,13 @@ BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, bool cap, int num
   const long long docs = std::max(s.docs, 1);
   const int kt = (s.kv_len + ltx::kBlockN - 1) / ltx::kBlockN;
   const int qt = (s.q_len + ltx::kBlockM - 1) / ltx::kBlockM;
-  f.units_kv = kt + s.docs;
-  f.units_q = qt + s.docs;
+  f.units_kv = max_units(s.kv_len, s.docs, ltx::kBlockN);
+  f.units_q = max_units(s.q_len, s.docs, ltx::kBlockM);
   const long long q_steps = (s.q_len / docs + ltx::kBlockM - 1) / ltx::kBlockM;
   const long long kv_steps = (s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN;
   f.parts_kv = plan_parts(std::max<long long>(kt, s.docs) * s.kv_heads * s.batch,
-                          q_steps * s.group, num_sms, 4);
-  f.parts_q = plan_parts(std::max<long long>(qt, s.docs) * s.heads * s.batch, kv_steps, num_sms,
-                         4);
+                          q_steps * s.group, num_sms);
+  f.parts_q = plan_parts(std::max<long long>(qt, s.docs) * s.heads * s.batch, kv_steps, num_sms);
   f.stat = ((size_t)s.batch * s.heads * s.q_len * sizeof(float2) + 15) / 16 * 16;
   const size_t row = (size_t)head_dim * sizeof(float);
   const size_t kv = f.parts_kv > 1
@@ -305,10 +311,8 @@ template <int D, bool kCap, bool kBias>
 cudaError_t launch_kv(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
                       cudaStream_t stream) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.kv_heads, p.s.batch, p.parts);
-  ltx::ltx_masked_bwd_kv<D, kCap, kBias>
-      <<<grid, ltx::kMaskedThreads, ltx::BwdKvSmem<D>::kAlloc, stream>>>(t.q, t.k, t.v, t.d_out,
-                                                                         p);
-  return cudaGetLastError();
+  return ltx::launch_dependent(ltx::ltx_masked_bwd_kv<D, kCap, kBias>, grid, ltx::kMaskedThreads,
+                               ltx::BwdKvSmem<D>::kAlloc, stream, t.q, t.k, t.v, t.d_out, p);
 }
 
 template <int D, bool kCap, bool kBias>
@@ -316,22 +320,19 @@ cudaError_t launch_q(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
                      cudaStream_t stream) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.heads, p.s.batch, p.parts);
   ltx::ltx_masked_bwd_q<D, kCap, kBias>
-      <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D, kCap>::kAlloc, stream>>>(t.q, t.k, t.v, t.d_out, p);
+      <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D, kCap>::kAlloc, stream>>>(t.q, t.k, t.v,
+                                                                              t.d_out, p);
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_sum(const ltx::MaskedBwdParams& p, const float* part, const float* fix,
-                       const float* e, const Tensor& out, const int* starts, int docs,
-                       cudaStream_t stream) {
-  const long long n = out.batch * out.heads * out.len * (D / 4);
-  ltx::ltx_masked_bwd_sum<D>
-      <<<(unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads), ltx::kCombineThreads,
-         0, stream>>>(part, fix, e, p.stat,
-                      static_cast<__nv_bfloat16*>(const_cast<void*>(out.base)), p.parts,
-                      (int)out.batch, (int)out.heads, (int)out.len, starts, docs, out.sb, out.sl,
-                      out.sh);
-  return cudaGetLastError();
+template <int D, bool kDq>
+cudaError_t launch_sum(const ltx::MaskedBwdParams& p, cudaStream_t stream) {
+  const long long rows = kDq ? (long long)p.s.batch * p.s.heads * p.s.q_len
+                             : 2LL * p.s.batch * p.s.kv_heads * p.s.kv_len;
+  const long long n = rows * (D / 4);
+  return ltx::launch_dependent(ltx::ltx_masked_bwd_sum<D, kDq>,
+                               (unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads),
+                               ltx::kCombineThreads, 0, stream, p);
 }
 
 void set_target(const Tensor& t, __nv_bfloat16** base, long long* stride) {
@@ -346,15 +347,12 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
                             const Tensor& d_out, const Tensor& dq, const Tensor& dk,
                             const Tensor& dv, const BwdMaps& maps, ltx::MaskedBwdParams p,
                             float* partials, cudaStream_t stream) {
-  ltx::ltx_masked_stat<D>
-      <<<dim3((unsigned)((a.q_len + ltx::kStatTokens - 1) / ltx::kStatTokens), (unsigned)a.heads,
-              (unsigned)a.batch),
-         256, 0, stream>>>(static_cast<const __nv_bfloat16*>(t.out.base),
-                           static_cast<const __nv_bfloat16*>(d_out.base), a.lse,
-                           p.stat, a.heads, a.q_len, t.out.sb, t.out.sl,
-                           t.out.sh, d_out.sb, d_out.sl, d_out.sh);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  __nv_bfloat16* base;
+  set_target(t.out, &base, p.out_stride);
+  p.out = base;
+  set_target(d_out, &base, p.d_out_stride);
+  p.d_out = base;
+  p.lse = a.lse;
   const bool cap = a.softcap > 0.0f, bias = a.slopes != nullptr;
   // dQ first: it leaves delta free of out's rounding
   p.parts = f.parts_q;
@@ -365,12 +363,13 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
     p.part1 = cap ? partials + rows * D : nullptr;
     p.part_e = partials + rows * D * (cap ? 2 : 1);
   }
-  e = cap ? (bias ? launch_q<D, true, true>(maps, p, f.units_q, stream)
+  cudaError_t e =
+      cap ? (bias ? launch_q<D, true, true>(maps, p, f.units_q, stream)
                   : launch_q<D, true, false>(maps, p, f.units_q, stream))
           : (bias ? launch_q<D, false, true>(maps, p, f.units_q, stream)
                   : launch_q<D, false, false>(maps, p, f.units_q, stream));
   if (e == cudaSuccess && p.parts > 1)
-    e = launch_sum<D>(p, p.part0, p.part1, p.part_e, dq, a.q_starts, a.docs, stream);
+    e = launch_sum<D, true>(p, stream);
   if (e != cudaSuccess) return e;
   // dK and dV
   p.parts = f.parts_kv;
@@ -385,11 +384,7 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
                   : launch_kv<D, true, false>(maps, p, f.units_kv, stream))
           : (bias ? launch_kv<D, false, true>(maps, p, f.units_kv, stream)
                   : launch_kv<D, false, false>(maps, p, f.units_kv, stream));
-  if (e == cudaSuccess && p.parts > 1) {
-    e = launch_sum<D>(p, p.part0, nullptr, nullptr, dk, a.kv_starts, a.docs, stream);
-    if (e == cudaSuccess)
-      e = launch_sum<D>(p, p.part1, nullptr, nullptr, dv, a.kv_starts, a.docs, stream);
-  }
+  if (e == cudaSuccess && p.parts > 1) e = launch_sum<D, false>(p, stream);
   return e;
 }
 

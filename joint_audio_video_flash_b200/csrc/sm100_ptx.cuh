@@ -595,6 +595,20 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // ----------------------------------------------------------------------------
+// programmatic dependent launch
+// ----------------------------------------------------------------------------
+// Waits until the grids this one depends on are complete and their writes visible; a no-op in
+// a kernel that was launched without the attribute.  Every thread of a dependent kernel calls
+// it ahead of its first access to global memory.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the grids that depend on this one start their CTAs where this grid leaves room.
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ----------------------------------------------------------------------------
 // arithmetic helpers
 // ----------------------------------------------------------------------------
 // Hardware base-2 exponential (MUFU.EX2), flush-to-zero; 2^-inf = 0.

@@ -446,9 +446,6 @@ ROPE_LAYOUTS = {"pairs": 0, "halves": 1}
 # The calls below run at the size of one token too, where the host's time is the call's time:
 # a tensor is looked at once, and the current device and stream are asked for once a call.
 
-_Strides = ctypes.c_longlong * 3
-
-
 @functools.lru_cache(maxsize=1)
 def _dtype_codes() -> dict:
     import torch
@@ -531,10 +528,10 @@ def _heads_strides(name: str, t, device: int, dtype, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
     if len(size) != 4 or 0 in size:
         raise ValueError(f"{name} must be a non-empty [batch, len, heads, head_dim] tensor")
-    sb, sl, sh, sd = t.stride()
-    if sd != 1 and size[3] > 1:
+    strides = t.stride()
+    if strides[3] != 1 and size[3] > 1:
         raise ValueError(f"the channels of {name} must be contiguous")
-    return _Strides(sb, sl, sh)
+    return strides[:3]
 
 
 def rope_frequencies(axis_dims, base: float = 10000.0) -> list[float]:
@@ -582,9 +579,9 @@ def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
         if pos_batch not in (1, batch) or positions.shape[1:] != (length, axes):
             raise ValueError(f"positions must be [{batch} or 1, {length}, {axes}]")
         if q_out is None:
-            q_out = torch.empty(shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q)
         q_out_strides = _heads_strides("q_out", q_out, device, q.dtype, shape)
-        kv_heads, k_strides, k_out_strides = 1, _Strides(), _Strides()
+        kv_heads, k_strides, k_out_strides = 1, (0, 0, 0), (0, 0, 0)
         if k is not None:
             k_strides = _heads_strides("k", k, device, None)
             k_shape = k.shape
@@ -593,7 +590,7 @@ def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
                 raise ValueError("k must have q's dtype, batch, length and head_dim")
             kv_heads = k_shape[2]
             if k_out is None:
-                k_out = torch.empty(k_shape, dtype=k.dtype, device=k.device)
+                k_out = torch.empty_like(k)
             k_out_strides = _heads_strides("k_out", k_out, device, k.dtype, k_shape)
         elif k_out is not None:
             raise ValueError("k_out without k")
@@ -672,7 +669,7 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps: float = 1e-6,
         code = _dtype_code(x)
         groups = _norm_affine(weight, bias, x, rows, cols, on.device)
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
             out_stride = cols
         else:
             out_stride = _norm_rows("out", out, on.device, x.dtype, x.shape)[2]
@@ -705,12 +702,15 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, *, stream=None)
         _check_cuda("rstd", rstd, device, torch.float32, stats)
         groups = _norm_affine(weight, None, x, rows, cols, device)
         if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dx_stride = _norm_rows("dx", dx, device, x.dtype, x.shape)[2]
+            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+            dx_stride = cols
+        else:
+            dx_stride = _norm_rows("dx", dx, device, x.dtype, x.shape)[2]
         dweight = dbias = workspace = None
         need = ctypes.c_ulonglong(0)
         if weight is not None:
-            dweight, dbias = torch.empty(2, *weight.shape, dtype=torch.float32, device=x.device)
+            dweight = torch.empty_like(weight, dtype=torch.float32)
+            dbias = torch.empty_like(dweight)
             _check(lib.ltxattn_layer_norm_workspace(rows, cols, groups, code,
                                                     ctypes.byref(need)),
                    "ltxattn_layer_norm_workspace")
@@ -758,7 +758,7 @@ def _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_star
         _check_cuda("slopes", slopes, device, torch.float32, (heads,))
     return _MaskedCall(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, q_strides, k_strides, v_strides,
-        _Strides(), batch, q_len, k_shape[1], heads, k_shape[2], head_dim,
+        (0, 0, 0), batch, q_len, k_shape[1], heads, k_shape[2], head_dim,
         1.0 / math.sqrt(head_dim) if scale is None else scale, softcap, _ptr(slopes),
         _ptr(prefix), _ptr(q_starts), _ptr(kv_starts), docs, bool(causal))
 
@@ -791,8 +791,7 @@ def masked_forward(q, k, v, out=None, lse=None, *, scale: float | None = None,
         call = _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_starts,
                             kv_starts)
         if out is None:  # rows of no document stay as they are made here
-            make = torch.empty if q_starts is None else torch.zeros
-            out = make(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q) if q_starts is None else torch.zeros_like(q)
         call.out_stride = _heads_strides("out", out, device, torch.bfloat16, q.shape)
         shape = (call.batch, call.heads, call.q_len)
         if lse is None:
@@ -829,11 +828,11 @@ def masked_backward(d_out, q, k, v, out, lse, dq=None, dk=None, dv=None, *,
         _check_cuda("lse", lse, device, torch.float32, (call.batch, call.heads, call.q_len))
         call.out, call.lse = out.data_ptr(), lse.data_ptr()
         d_out_strides = _heads_strides("d_out", d_out, device, bf16, q.shape)
-        make = torch.empty if q_starts is None else torch.zeros
+        make = torch.empty_like if q_starts is None else torch.zeros_like
         grads, strides = [], []
         for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             if t is None:
-                t = make(like.shape, dtype=bf16, device=like.device)
+                t = make(like)
             strides.append(_heads_strides(name, t, device, bf16, like.shape))
             grads.append(t)
         dq, dk, dv = grads
