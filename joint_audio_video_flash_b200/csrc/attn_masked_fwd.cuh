@@ -207,7 +207,8 @@ struct MaskedSmem {
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kDoc = kAbort + 4;
-  static constexpr int kUsed = kDoc + (int)sizeof(MaskedDoc);
+  static constexpr int kSums = kDoc + (int)sizeof(MaskedDoc);  // [2][128] fp32 (kFixed)
+  static constexpr int kUsed = kSums + 2 * kBlockM * 4;
   static constexpr int kRaw = ((kUsed + 1024 + 1023) / 1024) * 1024;
   static constexpr int kAlloc = kRaw > kMinSmemFor1Cta ? kRaw : kMinSmemFor1Cta;
   static_assert(kAlloc <= 227 * 1024, "shared memory of one SM");
@@ -253,6 +254,25 @@ __device__ __forceinline__ void masked_bias(float (&s)[N], const MaskedShape& p,
   }
 }
 
+// True when every product of the warp lies within the polynomial's range.  Whole warp.
+template <int N>
+__device__ __forceinline__ bool cap_within(const float (&s)[N], const MaskedShape& p) {
+  float lo = fmin3(s[0], s[1], s[2]);
+#pragma unroll
+  for (int c = 3; c + 1 < N; c += 2) lo = fmin3(lo, s[c], s[c + 1]);
+  lo = fminf(lo, s[N - 1]);
+  return !__any_sync(0xffffffffu, fmaxf(row_max<N>(s), -lo) > p.cap_limit);
+}
+
+// The capped scores of two products within the polynomial's range.
+__device__ __forceinline__ float2 cap_pair(float2 x, const MaskedShape& p) {
+  const float2 y = __fmul2_rn(x, x);
+  float2 r = make_float2(p.cap_poly[5], p.cap_poly[5]);
+#pragma unroll
+  for (int k = 4; k >= 0; --k) r = __ffma2_rn(r, y, make_float2(p.cap_poly[k], p.cap_poly[k]));
+  return __fmul2_rn(r, x);
+}
+
 // Turns a thread's N raw products into scores in log2 units when they are capped or biased;
 // far0 + dir * c is the distance of element c.  Whole warp.
 //
@@ -267,23 +287,13 @@ template <bool kCap, bool kBias, int N>
 __device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& p,
                                               float slope_log2, float far0, float dir) {
   if constexpr (kCap) {
-    float lo = fmin3(s[0], s[1], s[2]);
-#pragma unroll
-    for (int c = 3; c + 1 < N; c += 2) lo = fmin3(lo, s[c], s[c + 1]);
-    lo = fminf(lo, s[N - 1]);
-    if (__any_sync(0xffffffffu, fmaxf(row_max<N>(s), -lo) > p.cap_limit)) {
+    if (!cap_within(s, p)) {
 #pragma unroll
       for (int c = 0; c < N; ++c) s[c] = tanh_ex2(s[c] * p.cap_in) * p.cap_log2;
     } else {
 #pragma unroll
       for (int c = 0; c < N; c += 2) {
-        const float2 x = make_float2(s[c], s[c + 1]);
-        const float2 y = __fmul2_rn(x, x);
-        float2 r = make_float2(p.cap_poly[5], p.cap_poly[5]);
-#pragma unroll
-        for (int k = 4; k >= 0; --k)
-          r = __ffma2_rn(r, y, make_float2(p.cap_poly[k], p.cap_poly[k]));
-        r = __fmul2_rn(r, x);
+        const float2 r = cap_pair(make_float2(s[c], s[c + 1]), p);
         s[c] = r.x;
         s[c + 1] = r.y;
       }
@@ -292,13 +302,26 @@ __device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& 
   if constexpr (kBias) masked_bias<kCap>(s, p, slope_log2, far0, dir);
 }
 
-template <int D, bool kAlt, bool kCap, bool kBias>
+// The largest cap (log2 units) whose scores need no running maximum: weights 2^s between 2^-90
+// and 2^90 and sums of 2^24 of them are normal fp32 and bf16 numbers.
+constexpr float kFixedMaxCap = 90.0f;
+
+// kFixed (capped scores, cap <= kFixedMaxCap): the softmax runs without a maximum.  A row's
+// weights are 2^(s - m) with m = 0, or with a bias minus the bias of its nearest visible key,
+// known before any score is: no pass over the scores ahead of the exponentials, no rescaling
+// of O, and nothing that two threads would have to agree on before they use it.  So the two
+// softmax warpgroups share every tile, 64 keys each, instead of a tile each: a tile's softmax,
+// long because of the cap, takes half the time, and the tensor core has the other accumulator's
+// products to run meanwhile (8192 x 8192 x 16 heads x 128: TBD us; 750 us with a tile per
+// warpgroup, 780 us with a running maximum).
+template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>
 __global__ void __launch_bounds__(kMaskedThreads, 1)
     ltx_masked_fwd(const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ MaskedFwdParams p) {
   using L = MaskedSmem<D, kAlt>;
+  static_assert(!kFixed || kCap, "only a cap bounds the scores");
   constexpr bool kTransform = kCap || kBias;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -476,7 +499,9 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
           constexpr int kSteps = kBlockN / 16 / kMaskedPParts;
 #pragma unroll
           for (int kk = x * kSteps; kk < (x + 1) * kSteps; ++kk)
-            umma_ts_elect(tmem + L::kColO + D * g, tmem + L::kColS + 128 * g + kk * 8,
+            // kFixed: each half of P lies over the half of S that its warpgroup has read
+            umma_ts_elect(tmem + L::kColO + D * g,
+                          tmem + L::kColS + 128 * g + kk * 8 + (kFixed && kk >= 4 ? 32 : 0),
                           dv.at(v_off + kk * 16 * 128), idesc_pv, (step > 0 || kk > 0) ? 1u : 0u);
         }
         return true;
@@ -537,7 +562,93 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     float m_run = -INFINITY;
     float l_run = 0.0f;
     bool ok = !*abort_flag;
-    for (int step = 0; step < mine && ok; ++step) {
+    float* sums = reinterpret_cast<float*>(smem + L::kSums);
+    if constexpr (kFixed) {
+      // the keys [64 g, 64 g + 64) of both accumulators' tiles
+      int place_of[2], lim_of[2], lim_warp_of[2];
+      bool live_of[2];
+      float m_of[2], l_of[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int t0 = tok0 + (kAlt ? 0 : a * tile_tokens), query = t0 + row / pack;
+        place_of[a] = query + m.nk - m.nq;
+        lim_of[a] = masked_limit(m, p.s.causal, query);
+        lim_warp_of[a] = masked_limit(m, p.s.causal, t0 + (wq * 32) / pack);
+        live_of[a] = t0 + (wq * 32) / pack < m.nq;
+        m_of[a] = 0.0f;
+        if constexpr (kBias) {  // the nearest of the keys [0, lim)
+          const int far = place_of[a] < 0 ? -place_of[a] : max(place_of[a] - (lim_of[a] - 1), 0);
+          if (lim_of[a] > 0) m_of[a] = -slope * (float)far;
+        }
+      }
+      const int steps = max(n0, n1);
+      // one body for both accumulators and both chunks: unrolled, the two forms of the cap
+      // outgrow the instruction cache
+      for (int it = 0; it < 2 * steps && ok; ++it) {
+        const int a = it & 1, step = it >> 1;
+        if (step >= (a ? n1 : n0)) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::bSF + a), (uint32_t)step & 1u, ctl));
+        if (!ok) break;
+        tc_fence_after();
+        if (a ? live_of[1] : live_of[0]) {
+          const int kv0 = (begin + (kAlt ? it : step)) * kBlockN + g * 64;
+          const int place_a = (a ? place_of[1] : place_of[0]) - kv0;
+          const int to = (a ? lim_of[1] : lim_of[0]) - kv0;
+          const bool masked = kv0 + 64 > (a ? lim_warp_of[1] : lim_warp_of[0]);
+          const float top = a ? m_of[1] : m_of[0];
+          const uint32_t col = trow + L::kColS + 128 * a + g * 64;
+          float2 la = make_float2(0.0f, 0.0f), lb = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+          for (int c0 = 0; c0 < 64; c0 += 32) {
+            float v[32];
+            tmem_ld32(col + c0, v);
+            tmem_ld_wait_for(v);
+            uint32_t pk[16];
+            // scores to weights, pair by pair, so that the polynomials of some pairs run
+            // beside the exponentials of others
+            auto weights = [&](auto score) {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                const float2 t = score(x);
+                const float2 e = make_float2(ex2(t.x), ex2(t.y));
+                if (x & 1)
+                  lb = __fadd2_rn(lb, e);
+                else
+                  la = __fadd2_rn(la, e);
+                pk[x] = pack_bf16x2(e.x, e.y);
+              }
+            };
+            if (!kBias && !masked && cap_within(v, p.s)) {
+              weights([&](int x) { return cap_pair(make_float2(v[2 * x], v[2 * x + 1]), p.s); });
+            } else {
+              masked_scores<kCap, kBias>(v, p.s, slope, (float)(place_a - c0), -1.0f);
+              if (masked) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (c0 + c >= to) v[c] = -INFINITY;
+              }
+              weights([&](int x) {
+                return kBias ? make_float2(v[2 * x] - top, v[2 * x + 1] - top)
+                             : make_float2(v[2 * x], v[2 * x + 1]);
+              });
+            }
+            tmem_st16(col + c0 / 2, pk);
+          }
+          tmem_st_wait();
+          const float sum = (la.x + la.y) + (lb.x + lb.y);
+          l_of[0] += a ? 0.0f : sum;
+          l_of[1] += a ? sum : 0.0f;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bPF + g * 2 + a));
+      }
+      // the other warpgroup's share of this one's rows
+      sums[(1 - g) * kBlockM + row] = g ? l_of[0] : l_of[1];
+      m_run = g ? m_of[1] : m_of[0];
+      l_run = g ? l_of[1] : l_of[0];
+    }
+    for (int step = 0; !kFixed && step < mine && ok; ++step) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(L::bSF + g), (uint32_t)step & 1u, ctl));
       if (!ok) break;
       tc_fence_after();
@@ -609,6 +720,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     ok = named_bar_and(1, 256, ok && !*abort_flag);
     if (ok) {
       tc_fence_after();
+      if constexpr (kFixed) l_run += sums[g * kBlockM + row];
       float w_own = 1.0f, w_other = 0.0f;  // kAlt: weights of the two accumulators
       float* merge = reinterpret_cast<float*>(smem + L::kK);  // [D / 4][128] float4, then m, l
       if constexpr (kAlt) {
@@ -654,7 +766,8 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
             if (kAlt && n1 > 0) {
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
-                const float4 e = reinterpret_cast<const float4*>(merge)[(c * 8 + x) * kBlockM + row];
+                const float4 e = reinterpret_cast<const float4*>(
+                    merge)[(c * 8 + x) * kBlockM + row];
                 const float v4[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
                 for (int y = 0; y < 4; ++y)

@@ -236,11 +236,11 @@ size_t partial_bytes(const ltx::MaskedShape& s, int head_dim, int parts) {
   return parts > 1 ? (size_t)parts * s.batch * s.heads * s.q_len * (head_dim + 1) * 4 : 0;
 }
 
-template <int D, bool kAlt, bool kCap, bool kBias>
+template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>
 cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const ltx::MaskedFwdParams& p, int units, cudaStream_t stream) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.heads / p.s.pack, p.s.batch, p.parts);
-  ltx::ltx_masked_fwd<D, kAlt, kCap, kBias>
+  ltx::ltx_masked_fwd<D, kAlt, kCap, kBias, kFixed>
       <<<grid, ltx::kMaskedThreads, ltx::MaskedSmem<D, kAlt>::kAlloc, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
@@ -249,11 +249,14 @@ template <int D, bool kAlt>
 cudaError_t launch_fwd_scores(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const ltx::MaskedFwdParams& p, int units,
                               cudaStream_t stream) {
+  if (cap && p.s.cap_log2 <= ltx::kFixedMaxCap)
+    return bias ? launch_fwd<D, kAlt, true, true, true>(tq, tk, tv, p, units, stream)
+                : launch_fwd<D, kAlt, true, false, true>(tq, tk, tv, p, units, stream);
   if (cap)
-    return bias ? launch_fwd<D, kAlt, true, true>(tq, tk, tv, p, units, stream)
-                : launch_fwd<D, kAlt, true, false>(tq, tk, tv, p, units, stream);
-  return bias ? launch_fwd<D, kAlt, false, true>(tq, tk, tv, p, units, stream)
-              : launch_fwd<D, kAlt, false, false>(tq, tk, tv, p, units, stream);
+    return bias ? launch_fwd<D, kAlt, true, true, false>(tq, tk, tv, p, units, stream)
+                : launch_fwd<D, kAlt, true, false, false>(tq, tk, tv, p, units, stream);
+  return bias ? launch_fwd<D, kAlt, false, true, false>(tq, tk, tv, p, units, stream)
+              : launch_fwd<D, kAlt, false, false, false>(tq, tk, tv, p, units, stream);
 }
 
 template <int D>
@@ -408,19 +411,21 @@ cudaError_t set_bwd_scores() {
   return e;
 }
 
-template <int D, bool kAlt, bool kCap, bool kBias>
+template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>
 cudaError_t set_fwd() {
-  return cudaFuncSetAttribute(ltx::ltx_masked_fwd<D, kAlt, kCap, kBias>,
+  return cudaFuncSetAttribute(ltx::ltx_masked_fwd<D, kAlt, kCap, kBias, kFixed>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               ltx::MaskedSmem<D, kAlt>::kAlloc);
 }
 
 template <int D, bool kAlt>
 cudaError_t set_fwd_scores() {
-  cudaError_t e = set_fwd<D, kAlt, false, false>();
-  if (e == cudaSuccess) e = set_fwd<D, kAlt, false, true>();
-  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, false>();
-  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, true>();
+  cudaError_t e = set_fwd<D, kAlt, false, false, false>();
+  if (e == cudaSuccess) e = set_fwd<D, kAlt, false, true, false>();
+  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, false, false>();
+  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, true, false>();
+  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, false, true>();
+  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, true, true>();
   return e;
 }
 
