@@ -282,7 +282,7 @@ __device__ __forceinline__ float2 cap_pair(float2 x, const MaskedShape& p) {
 // cap tanh(s / cap) is an odd polynomial of degree 11 in packed fused multiply-adds, with a
 // largest error of 3.2e-7 cap in fp32 (the coefficients are a least-squares fit of tanh on
 // [-1, 1], reweighted until its ripples are level).
-// Measured at 8192 x 8192 x 16 heads x 128: TBD us against 1229 us with tanh_ex2 alone.
+// Measured at 8192 x 8192 x 16 heads x 128: 755 us against 1229 us with tanh_ex2 alone.
 template <bool kCap, bool kBias, int N>
 __device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& p,
                                               float slope_log2, float far0, float dir) {
@@ -307,13 +307,13 @@ __device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& 
 constexpr float kFixedMaxCap = 90.0f;
 
 // kFixed (capped scores, cap <= kFixedMaxCap): the softmax runs without a maximum.  A row's
-// weights are 2^(s - m) with m = 0, or with a bias minus the bias of its nearest visible key,
+// weights are 2^(s - m) with m = 0, or with a bias the largest bias of its visible keys,
 // known before any score is: no pass over the scores ahead of the exponentials, no rescaling
 // of O, and nothing that two threads would have to agree on before they use it.  So the two
 // softmax warpgroups share every tile, 64 keys each, instead of a tile each: a tile's softmax,
 // long because of the cap, takes half the time, and the tensor core has the other accumulator's
-// products to run meanwhile (8192 x 8192 x 16 heads x 128: TBD us; 750 us with a tile per
-// warpgroup, 780 us with a running maximum).
+// products to run meanwhile (8192 x 8192 x 16 heads x 128: 690 us; 790 us with a running maximum
+// and a tile per warpgroup, 485 us without a cap).
 template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>
 __global__ void __launch_bounds__(kMaskedThreads, 1)
     ltx_masked_fwd(const __grid_constant__ CUtensorMap tm_q,
@@ -576,8 +576,12 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         lim_warp_of[a] = masked_limit(m, p.s.causal, t0 + (wq * 32) / pack);
         live_of[a] = t0 + (wq * 32) / pack < m.nq;
         m_of[a] = 0.0f;
-        if constexpr (kBias) {  // the nearest of the keys [0, lim)
-          const int far = place_of[a] < 0 ? -place_of[a] : max(place_of[a] - (lim_of[a] - 1), 0);
+        if constexpr (kBias) {  // of the keys [0, lim): the nearest, or with a negative slope the
+                                // farthest, has the largest bias
+          const int first = place_of[a], last = place_of[a] - (lim_of[a] - 1);
+          const int far = slope < 0.0f              ? max(abs(first), abs(last))
+                          : first >= 0 && last <= 0 ? 0
+                                                    : min(abs(first), abs(last));
           if (lim_of[a] > 0) m_of[a] = -slope * (float)far;
         }
       }
@@ -598,11 +602,14 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
           const float top = a ? m_of[1] : m_of[0];
           const uint32_t col = trow + L::kColS + 128 * a + g * 64;
           float2 la = make_float2(0.0f, 0.0f), lb = make_float2(0.0f, 0.0f);
-#pragma unroll 1
+          float both[2][32];
+          tmem_ld32(col, both[0]);
+          tmem_ld32(col + 32, both[1]);
+          tmem_ld_wait_for(both[0]);
+          tmem_ld_wait_for(both[1]);
+#pragma unroll
           for (int c0 = 0; c0 < 64; c0 += 32) {
-            float v[32];
-            tmem_ld32(col + c0, v);
-            tmem_ld_wait_for(v);
+            float(&v)[32] = both[c0 / 32];
             uint32_t pk[16];
             // scores to weights, pair by pair, so that the polynomials of some pairs run
             // beside the exponentials of others

@@ -128,7 +128,7 @@ def masked(q, k, v, scale=None, softcap=0.0, slopes=None, causal=False, prefix=N
                     s_mag = s_mag.clamp(max=softcap) + softcap
                 if slopes is not None:
                     far = float(slopes[h]) * (i - j).abs()
-                    s, s_mag = s - far, s_mag + far
+                    s, s_mag = s - far, s_mag + far.abs()  # a magnitude, whatever the sign
                 s = s.masked_fill(~seen, -math.inf)
                 top = s.amax(1, keepdim=True) if nk else torch.full((nq, 1), -math.inf).double()
                 top = torch.where(top == -math.inf, 0.0, top)

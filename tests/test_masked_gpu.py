@@ -280,6 +280,19 @@ def test_scores_of_every_size():
     compare(run(q, k, v, opts), block_ops.masked(q, k, v, **opts), ("out", "lse"))
 
 
+@pytest.mark.parametrize("cap", [0.0, 6.0, 62.0, 63.0, 500.0])
+def test_every_cap_and_slopes_of_both_signs(cap):
+    # caps on either side of the form without a maximum; slopes that favour far keys; a query
+    # stretch that lies wholly ahead of or behind its keys
+    for q_len, kv_len, causal in ((200, 170, False), (90, 400, True), (400, 90, False)):
+        q, k, v, d_out = make(1, q_len, kv_len, 4, 2, 64, seed=3)
+        for slopes in ([0.5, 0.01, -0.02, -0.4], [3.0, 0.0, -3.0, 1e-4]):
+            opts = dict(softcap=cap, slopes=torch.tensor(slopes), causal=causal, scale=0.6)
+            ref = block_ops.masked(q, k, v, d_out=d_out, **opts)
+            compare(run(q, k, v, opts), ref, ("out", "lse"))
+            compare(run_backward(q, k, v, d_out, opts), ref, ("dq", "dk", "dv"))
+
+
 def test_strided_views_and_layouts():
     g = torch.Generator().manual_seed(4)
     qkv = torch.randn(2, 150, 8 + 2 * 2, 64, generator=g).bfloat16()
