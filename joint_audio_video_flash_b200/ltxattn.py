@@ -12,6 +12,7 @@ import functools
 import math
 import os
 import re
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -64,6 +65,25 @@ class _MaskedGrad(ctypes.Structure):
                    for n in ("d_out_stride", "dq_stride", "dk_stride", "dv_stride")])
 
 
+def _packer(cls):
+    """``struct.Struct`` of a ctypes structure's fields, arrays spelled out: packing a call's
+    arguments into bytes takes a third of the time of filling the structure."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_longlong: "q", ctypes.c_int: "i",
+             ctypes.c_float: "f"}
+    fmt = "@"
+    for _, kind in cls._fields_:
+        if issubclass(kind, ctypes.Array):
+            fmt += f"{kind._length_}{codes[kind._type_]}"
+        else:
+            fmt += codes.get(kind, "P")
+    packer = struct.Struct(fmt)
+    assert packer.size <= ctypes.sizeof(cls)  # a trailing pad at most
+    return packer.pack
+
+
+_pack_rope, _pack_masked, _pack_grad = (_packer(c) for c in (_RopeCall, _MaskedCall, _MaskedGrad))
+
+
 def load() -> ctypes.CDLL:
     """Load libltxattn.so (built by ``joint_audio_video_flash_b200.build``); raise if absent."""
     global _lib
@@ -93,16 +113,14 @@ def load() -> ctypes.CDLL:
             lib.ltxattn_combine.argtypes = [vp, vp, vp] + [ci] * 5 + [vp]
             lib.ltxattn_forward_grouped.argtypes = [vp, ci, vp]
             ll, ull = ctypes.c_longlong, ctypes.c_ulonglong
-            lib.ltxattn_rope_axes.argtypes = [ctypes.POINTER(_RopeCall), vp]
+            lib.ltxattn_rope_axes.argtypes = [vp, vp]  # the structs: packed bytes
             lib.ltxattn_layer_norm.argtypes = [vp] * 6 + [ll, ci, ll, ll, ll, cf, ci, vp]
             lib.ltxattn_layer_norm_workspace.argtypes = [ll, ci, ll, ci, ctypes.POINTER(ull)]
             lib.ltxattn_layer_norm_backward.argtypes = ([vp] * 8 + [ll, ci] + [ll] * 4
                                                         + [ci, vp, ull, vp])
-            lib.ltxattn_masked_forward.argtypes = [ctypes.POINTER(_MaskedCall), vp, ull, vp]
-            lib.ltxattn_masked_backward.argtypes = [ctypes.POINTER(_MaskedCall),
-                                                    ctypes.POINTER(_MaskedGrad), vp, ull, vp]
-            lib.ltxattn_masked_workspace.argtypes = [ctypes.POINTER(_MaskedCall), ci,
-                                                     ctypes.POINTER(ull)]
+            lib.ltxattn_masked_forward.argtypes = [vp, vp, ull, vp]
+            lib.ltxattn_masked_backward.argtypes = [vp, vp, vp, ull, vp]
+            lib.ltxattn_masked_workspace.argtypes = [vp, ci, ctypes.POINTER(ull)]
             lib.ltxattn_entry_point_name.argtypes = [ci]
             lib.ltxattn_entry_point_name.restype = ctypes.c_char_p
             _lib = lib
@@ -543,13 +561,14 @@ def rope_frequencies(axis_dims, base: float = 10000.0) -> list[float]:
 
 @functools.lru_cache(maxsize=16)
 def _rope_axes_arrays(inv_freq: tuple, axis_dims: tuple):
-    """The C arrays of these numbers."""
+    """The frequencies as a C array, its address, and four axes' channels."""
     dims = tuple(int(x) for x in axis_dims)
     if not 1 <= len(dims) <= 4:
         raise ValueError("axis_dims must name one to four axes")
     if len(inv_freq) != sum(dims) // 2:
         raise ValueError(f"{len(inv_freq)} frequencies for {sum(dims) // 2} rotated pairs")
-    return (ctypes.c_double * len(inv_freq))(*inv_freq), (ctypes.c_int * 4)(*dims)
+    freq = (ctypes.c_double * len(inv_freq))(*inv_freq)
+    return freq, ctypes.addressof(freq), dims + (0,) * (4 - len(dims))
 
 
 def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
@@ -563,7 +582,7 @@ def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
     the gradient.  The outputs may be the inputs (in place).
     """
     import torch
-    freq, dims = _rope_axes_arrays(tuple(inv_freq), tuple(axis_dims))
+    freq, freq_at, dims = _rope_axes_arrays(tuple(inv_freq), tuple(axis_dims))
     axes = len(axis_dims)
     code_layout = ROPE_LAYOUTS.get(layout)
     if code_layout is None:
@@ -594,10 +613,10 @@ def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
             k_out_strides = _heads_strides("k_out", k_out, device, k.dtype, k_shape)
         elif k_out is not None:
             raise ValueError("k_out without k")
-        call = _RopeCall(
-            q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-            None if k is None else k_out.data_ptr(), q_strides, k_strides, q_out_strides,
-            k_out_strides, positions.data_ptr(), freq, dims, axes, pos_batch, batch, length,
+        call = _pack_rope(
+            q.data_ptr(), 0 if k is None else k.data_ptr(), q_out.data_ptr(),
+            0 if k is None else k_out.data_ptr(), *q_strides, *k_strides, *q_out_strides,
+            *k_out_strides, positions.data_ptr(), freq_at, *dims, axes, pos_batch, batch, length,
             heads, kv_heads, head_dim, code, code_layout, bool(inverse))
         _check(load().ltxattn_rope_axes(call, on.handle), "ltxattn_rope_axes")
         on.used(q, k, q_out, k_out, positions)
@@ -729,18 +748,20 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_starts, kv_starts):
-    """Checks what the library cannot see from raw pointers; returns the _MaskedCall, out and
-    lse not filled in."""
+def _masked_call(device, q, k, v, out, lse, scale, softcap, slopes, causal, prefix, q_starts,
+                 kv_starts) -> bytes:
+    """Checks what the library cannot see from raw pointers; returns the ltxattn_masked_call."""
     import torch
     bf16 = torch.bfloat16
     q_strides = _heads_strides("q", q, device, bf16)
     k_strides = _heads_strides("k", k, device, bf16)
-    batch, q_len, heads, head_dim = q.shape
-    k_shape = k.shape
+    q_shape, k_shape = q.shape, k.shape
+    batch, q_len, heads, head_dim = q_shape
     if k_shape[0] != batch or k_shape[3] != head_dim or v.shape != k_shape:
         raise ValueError("k and v must be [batch, kv_len, kv_heads, head_dim] matching q")
     v_strides = _heads_strides("v", v, device, bf16)
+    out_strides = _heads_strides("out", out, device, bf16, q_shape)
+    _check_cuda("lse", lse, device, torch.float32, (batch, heads, q_len))
     docs = 0
     if q_starts is not None or kv_starts is not None:
         if q_starts is None or kv_starts is None:
@@ -756,19 +777,22 @@ def _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_star
         _check_cuda("prefix", prefix, device, torch.int32, (batch, max(docs, 1)))
     if slopes is not None:
         _check_cuda("slopes", slopes, device, torch.float32, (heads,))
-    return _MaskedCall(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, q_strides, k_strides, v_strides,
-        (0, 0, 0), batch, q_len, k_shape[1], heads, k_shape[2], head_dim,
-        1.0 / math.sqrt(head_dim) if scale is None else scale, softcap, _ptr(slopes),
-        _ptr(prefix), _ptr(q_starts), _ptr(kv_starts), docs, bool(causal))
+    return _pack_masked(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *q_strides,
+        *k_strides, *v_strides, *out_strides, batch, q_len, k_shape[1], heads, k_shape[2],
+        head_dim, 1.0 / math.sqrt(head_dim) if scale is None else scale, softcap,
+        0 if slopes is None else slopes.data_ptr(), 0 if prefix is None else prefix.data_ptr(),
+        0 if docs == 0 else q_starts.data_ptr(), 0 if docs == 0 else kv_starts.data_ptr(), docs,
+        bool(causal))
 
 
-def _masked_workspace(call, backward: bool, device):
+def _masked_workspace(lib, call, backward: bool, device):
+    """Workspace of the call, and its bytes."""
     import torch
     need = ctypes.c_ulonglong(0)
-    _check(load().ltxattn_masked_workspace(call, backward, ctypes.byref(need)),
-           "ltxattn_masked_workspace")
-    return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+    _check(lib.ltxattn_masked_workspace(call, backward, need), "ltxattn_masked_workspace")
+    n = need.value
+    return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
 
 
 def masked_forward(q, k, v, out=None, lse=None, *, scale: float | None = None,
@@ -787,22 +811,21 @@ def masked_forward(q, k, v, out=None, lse=None, *, scale: float | None = None,
     """
     import torch
     with _OnStream(stream) as on:
-        device = on.device
-        call = _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_starts,
-                            kv_starts)
-        if out is None:  # rows of no document stay as they are made here
-            out = torch.empty_like(q) if q_starts is None else torch.zeros_like(q)
-        call.out_stride = _heads_strides("out", out, device, torch.bfloat16, q.shape)
-        shape = (call.batch, call.heads, call.q_len)
-        if lse is None:
-            lse = torch.empty(shape, dtype=torch.float32, device=q.device) if q_starts is None \
-                else torch.full(shape, -math.inf, dtype=torch.float32, device=q.device)
-        else:
-            _check_cuda("lse", lse, device, torch.float32, shape)
-        call.out, call.lse = out.data_ptr(), lse.data_ptr()
-        workspace = _masked_workspace(call, False, q.device)
-        _check(load().ltxattn_masked_forward(
-            call, _ptr(workspace), 0 if workspace is None else workspace.numel(), on.handle),
+        if out is None or lse is None:  # rows of no document stay as they are made here
+            _heads_strides("q", q, on.device, torch.bfloat16)
+            if out is None:
+                out = torch.empty_like(q) if q_starts is None else torch.zeros_like(q)
+            if lse is None:
+                shape = (q.shape[0], q.shape[2], q.shape[1])
+                lse = torch.empty(shape, dtype=torch.float32, device=q.device) \
+                    if q_starts is None else \
+                    torch.full(shape, -math.inf, dtype=torch.float32, device=q.device)
+        call = _masked_call(on.device, q, k, v, out, lse, scale, softcap, slopes, causal, prefix,
+                            q_starts, kv_starts)
+        lib = load()
+        workspace, need = _masked_workspace(lib, call, False, q.device)
+        _check(lib.ltxattn_masked_forward(
+            call, None if workspace is None else workspace.data_ptr(), need, on.handle),
             "ltxattn_masked_forward")
         on.used(q, k, v, out, lse, slopes, prefix, q_starts, kv_starts)
     return out, lse
@@ -822,11 +845,8 @@ def masked_backward(d_out, q, k, v, out, lse, dq=None, dk=None, dv=None, *,
         raise ValueError("out and lse of the forward call are needed")
     with _OnStream(stream) as on:
         device, bf16 = on.device, torch.bfloat16
-        call = _masked_call(device, q, k, v, scale, softcap, slopes, causal, prefix, q_starts,
-                            kv_starts)
-        call.out_stride = _heads_strides("out", out, device, bf16, q.shape)
-        _check_cuda("lse", lse, device, torch.float32, (call.batch, call.heads, call.q_len))
-        call.out, call.lse = out.data_ptr(), lse.data_ptr()
+        call = _masked_call(device, q, k, v, out, lse, scale, softcap, slopes, causal, prefix,
+                            q_starts, kv_starts)
         d_out_strides = _heads_strides("d_out", d_out, device, bf16, q.shape)
         make = torch.empty_like if q_starts is None else torch.zeros_like
         grads, strides = [], []
@@ -836,11 +856,11 @@ def masked_backward(d_out, q, k, v, out, lse, dq=None, dk=None, dv=None, *,
             strides.append(_heads_strides(name, t, device, bf16, like.shape))
             grads.append(t)
         dq, dk, dv = grads
-        grad = _MaskedGrad(d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                           d_out_strides, *strides)
-        workspace = _masked_workspace(call, True, q.device)
-        _check(load().ltxattn_masked_backward(call, grad, workspace.data_ptr(),
-                                              workspace.numel(), on.handle),
+        grad = _pack_grad(d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                          *d_out_strides, *strides[0], *strides[1], *strides[2])
+        lib = load()
+        workspace, need = _masked_workspace(lib, call, True, q.device)
+        _check(lib.ltxattn_masked_backward(call, grad, workspace.data_ptr(), need, on.handle),
                "ltxattn_masked_backward")
         on.used(d_out, q, k, v, out, lse, dq, dk, dv, slopes, prefix, q_starts, kv_starts)
     return dq, dk, dv
