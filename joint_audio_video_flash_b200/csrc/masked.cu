@@ -216,20 +216,41 @@ int plan_parts(long long ctas, long long steps, int num_sms) {
   return parts;
 }
 
-// One tile of queries per document (on average) runs the alternating form: with one tile, the
-// base form's second accumulator would idle.
-FwdPlan plan_forward(const ltx::MaskedShape& s, int num_sms) {
-  FwdPlan f;
+// Chooses the form and the key parts with the least expected time, in tenths of a microsecond:
+// waves of CTAs x (start and end of a CTA + its key tiles x time per tile), and for parts the
+// merge with its partials' traffic.  The times are measured ones (8192 x 8192 x 16 heads, and
+// one tile alone): a key tile takes the base form, two query tiles, 1.9 us at head_dim 128 and
+// 1.7 at 64, the alternating form 1.2 and 1.0 us for its one.  So the base form has the long
+// cases (8192 x 8192 x 16 x 128: 490 us against 543) and the alternating form those that leave
+// SMs without work (2048 x 2048 x 8 x 128: 25 us against 38) and single query tiles.
+FwdPlan plan_forward(const ltx::MaskedShape& s, int head_dim, int num_sms) {
   const long long docs = std::max(s.docs, 1);
-  f.alt = (long long)s.q_len * s.pack <= docs * ltx::kBlockM;
-  const int rows = ltx::kBlockM / s.pack * (f.alt ? 1 : 2);
-  f.units = max_units(s.q_len, s.docs, rows);
-  // units that hold rows, as far as the host can tell
-  const long long filled = std::max<long long>((s.q_len + rows - 1) / rows, s.docs);
-  const long long ctas = filled * (s.heads / s.pack) * s.batch;
-  const long long tiles = (s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN;
-  f.parts = plan_parts(ctas, tiles, num_sms);
-  return f;
+  const long long tiles = std::max<long long>(
+      1, (s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN);
+  const long long per_head = (long long)(s.heads / s.pack) * s.batch;
+  // partials written and read at 6 TB/s
+  const long long part_bytes = (long long)s.batch * s.heads * s.q_len * (head_dim + 1) * 8;
+  FwdPlan best{};
+  long long best_cost = -1;
+  for (const bool alt : {false, true}) {
+    const int rows = ltx::kBlockM / s.pack * (alt ? 1 : 2);
+    const long long tile_time = head_dim == 128 ? (alt ? 12 : 19) : (alt ? 10 : 17);
+    const int units = max_units(s.q_len, s.docs, rows);
+    // units that will hold rows: a document's last one is half full on average
+    const long long filled =
+        std::min<long long>(units, (2LL * s.q_len + (long long)s.docs * rows) / (2 * rows) + 1);
+    for (int parts = 1; parts <= (int)std::min<long long>(tiles, 64); ++parts) {
+      if (parts > 1 && filled * per_head >= num_sms) break;
+      const long long waves = (filled * per_head * parts + num_sms - 1) / num_sms;
+      long long cost = waves * (70 + tile_time * ((tiles + parts - 1) / parts));
+      if (parts > 1) cost += 40 + parts * part_bytes / 600000;
+      if (best_cost < 0 || cost < best_cost) {
+        best_cost = cost;
+        best = FwdPlan{alt, units, parts};
+      }
+    }
+  }
+  return best;
 }
 
 size_t partial_bytes(const ltx::MaskedShape& s, int head_dim, int parts) {
@@ -460,7 +481,7 @@ int ltxattn_masked_workspace(const ltxattn_masked_call* call, int backward,
     const BwdPlan f = plan_backward(s, call->head_dim, call->softcap > 0.0f, c.num_sms);
     *bytes = f.stat + f.partials;
   } else {
-    *bytes = partial_bytes(s, call->head_dim, plan_forward(s, c.num_sms).parts);
+    *bytes = partial_bytes(s, call->head_dim, plan_forward(s, call->head_dim, c.num_sms).parts);
   }
   return LTXATTN_OK;
 }
@@ -491,7 +512,7 @@ int ltxattn_masked_forward(const ltxattn_masked_call* call, void* workspace,
   p.out_stride[1] = t.out.sl;
   p.out_stride[2] = t.out.sh;
   p.lse = a.lse;
-  const FwdPlan f = plan_forward(p.s, c.num_sms);
+  const FwdPlan f = plan_forward(p.s, a.head_dim, c.num_sms);
   p.parts = f.parts;
   if (grid_ctas(f.units, a.heads / p.s.pack, a.batch, f.parts) > kMaxCtas)
     return LTXATTN_ERR_UNSUPPORTED;
