@@ -11,12 +11,14 @@
 // where the softmax is peaked.  ltx_masked_bwd_q, which runs first, sums
 // e_i = sum_j P_ij (dP_ij - delta_i) in fp32 on its way: delta_i + e_i is free of out's rounding,
 // and that is what ltx_masked_bwd_kv gets.  dQ's own share of the error is -e_i sum_j P_ij b_ij
-// K_j (b the cap's derivative).  With a cap (kCap), which is there because scores are large, the
-// kernel carries that sum as a second accumulator and takes it out: the softmax's arithmetic
-// bounds it there, so the product is nearly free.  Without a cap it would add a third to the
-// bound of the kernel for errors that scores of ordinary size do not show (measured against 64
-// bits, relative to the gradient's norm: dQ 2.4e-3 without it at N(0, 1) scores, of which 1.7e-3
-// is the rounding of the result; capped scores of deviation 4: 3.6e-3 without, 2.4e-3 with it).
+// K_j (b the cap's derivative).  With kFix the kernel carries that sum as a second accumulator
+// and takes it out.  The host asks for it with a cap (which is there because scores are large;
+// the softmax's arithmetic bounds the kernel then, and the product is nearly free), with a bias
+// (which gathers the weight on the near keys) and for rows of few keys.  For long rows of plain
+// scores it would add a third to the kernel's bound for an error that does not show: measured
+// against 64 bits, relative to the gradient's norm, dQ is 2.4e-3 off without it at 7680 keys and
+// N(0, 1) scores, of which 1.7e-3 is the rounding of the result; at 16 keys 2.7e-3 without, and
+// with capped scores of deviation 4 3.6e-3 without and 2.4e-3 with it.
 //
 // Two kernels instead of one: ltx_masked_bwd_kv owns a tile of 128 keys and walks the queries
 // that see it (dK and dV stay in TMEM, the query heads that share the key head one after the
@@ -59,7 +61,7 @@ struct MaskedBwdParams {
   __nv_bfloat16* d1;   // dV
   long long stride0[3], stride1[3];  // batch, token, head
   float* part0;        // [parts][batch][heads | kv_heads][len][D]: dQ or dK
-  float* part1;        // dV; sum P b K (dQ with a cap)
+  float* part1;        // dV; sum P b K (dQ, kFix)
   float* part_e;       // [parts][batch][heads][len]: e (dQ)
 };
 
@@ -598,14 +600,13 @@ struct BwdQSmem {
   static constexpr uint32_t kTmemCols = 512;
 };
 
-template <int D, bool kCap, bool kBias>
+template <int D, bool kCap, bool kBias, bool kFix>
 __global__ void __launch_bounds__(kMaskedThreads, 1)
     ltx_masked_bwd_q(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ MaskedBwdParams p) {
-  constexpr bool kFix = kCap;
   using L = BwdQSmem<D, kFix>;
   constexpr int kSBuf = L::kSBuf;
   extern __shared__ uint8_t smem_raw[];
@@ -887,8 +888,9 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x)
-            pk[x] = pack_bf16x2(s[c * 32 + 2 * x] * bent[c * 32 + 2 * x],
-                                s[c * 32 + 2 * x + 1] * bent[c * 32 + 2 * x + 1]);
+            pk[x] = kCap ? pack_bf16x2(s[c * 32 + 2 * x] * bent[c * 32 + 2 * x],
+                                       s[c * 32 + 2 * x + 1] * bent[c * 32 + 2 * x + 1])
+                         : pack_bf16x2(s[c * 32 + 2 * x], s[c * 32 + 2 * x + 1]);
           tmem_st16(trow + L::kColS + g * 64 + c * 16, pk);
         }
         tmem_st_wait();

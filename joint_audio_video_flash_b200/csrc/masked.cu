@@ -165,11 +165,12 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
     s.cap_log2 = a.softcap * kLog2e;
     // tanh(x) = x P(x^2) on [-1, 1], rescaled to take raw products; where a coefficient would
     // leave the normal fp32 range the limit of 0 leaves every product to the general form
-    const double tanh_poly[6] = {0.9999968409538269,   -0.3332400321960449,
-                                 0.13253524899482727,  -0.05097284913063049,
-                                 0.016114167869091034, -0.0028394602704793215};
+    const double tanh_poly[7] = {0.9999997019767761, -0.33332130312919617,
+                                 0.13319583237171173, -0.053265832364559174,
+                                 0.019973276183009148, -0.005951274652034044,
+                                 0.0009637702605687082};
     s.cap_limit = 1.0f / s.cap_in;
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < 7; ++i) {
       const double c = tanh_poly[i] * (double)s.cap_log2 * std::pow((double)s.cap_in, 2 * i + 1);
       s.cap_poly[i] = (float)c;
       if (!(std::fabs(c) > 1e-37 && std::fabs(c) < 1e37)) s.cap_limit = 0.0f;
@@ -180,6 +181,14 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
   s.timeout_ns = kTimeoutNs;
   return s;
 }
+
+// Rows of few keys (per document, on average) have the forms that lose least where one key has
+// most of a row's weight: a running maximum with a cap, and dQ free of out's rounding without
+// one.  Their time is latency, not arithmetic (2 x 1003 keys, 12 heads of 64, causal: forward 42 us
+// with either form, backward 79 to 85 us with it and 75 to 86 us without); at 8192 keys the
+// maximum costs a capped forward call 790 us instead of 700, and the sum a plain backward a third.
+constexpr int kFewKeys = 2048;
+bool few_keys(const ltx::MaskedShape& s) { return s.kv_len / std::max(s.docs, 1) <= kFewKeys; }
 
 long long grid_ctas(int units, int heads, int batch, int parts) {
   return (long long)units * heads * batch * parts;
@@ -270,7 +279,7 @@ template <int D, bool kAlt>
 cudaError_t launch_fwd_scores(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const ltx::MaskedFwdParams& p, int units,
                               cudaStream_t stream) {
-  if (cap && p.s.cap_log2 <= ltx::kFixedMaxCap)
+  if (cap && p.s.cap_log2 <= ltx::kFixedMaxCap && !few_keys(p.s))
     return bias ? launch_fwd<D, kAlt, true, true, true>(tq, tk, tv, p, units, stream)
                 : launch_fwd<D, kAlt, true, false, true>(tq, tk, tv, p, units, stream);
   if (cap)
@@ -303,7 +312,10 @@ struct BwdPlan {
   size_t stat, partials;  // bytes of workspace
 };
 
-// cap: dQ's parts carry the second accumulator too.
+// Whether the dQ kernel carries the sum that takes out's rounding off dQ (attn_masked_bwd.cuh):
+// where scores are capped or biased, or rows have few keys.
+bool dq_fix(const ltx::MaskedShape& s, bool cap) { return cap || s.slopes || few_keys(s); }
+
 BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, bool cap, int num_sms) {
   BwdPlan f;
   const long long docs = std::max(s.docs, 1);
@@ -321,7 +333,7 @@ BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, bool cap, int num
   const size_t kv = f.parts_kv > 1
                         ? 2 * (size_t)f.parts_kv * s.batch * s.kv_heads * s.kv_len * row : 0;
   const size_t q = f.parts_q > 1 ? (size_t)f.parts_q * s.batch * s.heads * s.q_len *
-                                       ((cap ? 2 : 1) * row + sizeof(float))
+                                       ((dq_fix(s, cap) ? 2 : 1) * row + sizeof(float))
                                  : 0;
   f.partials = std::max(kv, q);  // used one after the other
   return f;
@@ -339,12 +351,12 @@ cudaError_t launch_kv(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units
                                ltx::BwdKvSmem<D>::kAlloc, stream, t.q, t.k, t.v, t.d_out, p);
 }
 
-template <int D, bool kCap, bool kBias>
+template <int D, bool kCap, bool kBias, bool kFix>
 cudaError_t launch_q(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
                      cudaStream_t stream) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.heads, p.s.batch, p.parts);
-  ltx::ltx_masked_bwd_q<D, kCap, kBias>
-      <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D, kCap>::kAlloc, stream>>>(t.q, t.k, t.v,
+  ltx::ltx_masked_bwd_q<D, kCap, kBias, kFix>
+      <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D, kFix>::kAlloc, stream>>>(t.q, t.k, t.v,
                                                                               t.d_out, p);
   return cudaGetLastError();
 }
@@ -377,21 +389,22 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
   set_target(d_out, &base, p.d_out_stride);
   p.d_out = base;
   p.lse = a.lse;
-  const bool cap = a.softcap > 0.0f, bias = a.slopes != nullptr;
+  const bool cap = a.softcap > 0.0f, bias = a.slopes != nullptr, fix = dq_fix(p.s, cap);
   // dQ first: it leaves delta free of out's rounding
   p.parts = f.parts_q;
   set_target(dq, &p.d0, p.stride0);
   if (p.parts > 1) {
     const size_t rows = (size_t)p.parts * a.batch * a.heads * a.q_len;
     p.part0 = partials;
-    p.part1 = cap ? partials + rows * D : nullptr;
-    p.part_e = partials + rows * D * (cap ? 2 : 1);
+    p.part1 = fix ? partials + rows * D : nullptr;
+    p.part_e = partials + rows * D * (fix ? 2 : 1);
   }
   cudaError_t e =
-      cap ? (bias ? launch_q<D, true, true>(maps, p, f.units_q, stream)
-                  : launch_q<D, true, false>(maps, p, f.units_q, stream))
-          : (bias ? launch_q<D, false, true>(maps, p, f.units_q, stream)
-                  : launch_q<D, false, false>(maps, p, f.units_q, stream));
+      cap ? (bias ? launch_q<D, true, true, true>(maps, p, f.units_q, stream)
+                  : launch_q<D, true, false, true>(maps, p, f.units_q, stream))
+          : (bias  ? launch_q<D, false, true, true>(maps, p, f.units_q, stream)
+             : fix ? launch_q<D, false, false, true>(maps, p, f.units_q, stream)
+                   : launch_q<D, false, false, false>(maps, p, f.units_q, stream));
   if (e == cudaSuccess && p.parts > 1)
     e = launch_sum<D, true>(p, stream);
   if (e != cudaSuccess) return e;
@@ -413,22 +426,30 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
 }
 
 template <int D, bool kCap, bool kBias>
-cudaError_t set_bwd() {
-  cudaError_t e = cudaFuncSetAttribute(ltx::ltx_masked_bwd_kv<D, kCap, kBias>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       ltx::BwdKvSmem<D>::kAlloc);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, kCap, kBias>,
+cudaError_t set_bwd_kv() {
+  return cudaFuncSetAttribute(ltx::ltx_masked_bwd_kv<D, kCap, kBias>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ltx::BwdQSmem<D, kCap>::kAlloc);
+                              ltx::BwdKvSmem<D>::kAlloc);
+}
+
+template <int D, bool kCap, bool kBias, bool kFix>
+cudaError_t set_bwd_q() {
+  return cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, kCap, kBias, kFix>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              ltx::BwdQSmem<D, kFix>::kAlloc);
 }
 
 template <int D>
 cudaError_t set_bwd_scores() {
-  cudaError_t e = set_bwd<D, false, false>();
-  if (e == cudaSuccess) e = set_bwd<D, false, true>();
-  if (e == cudaSuccess) e = set_bwd<D, true, false>();
-  if (e == cudaSuccess) e = set_bwd<D, true, true>();
+  cudaError_t e = set_bwd_kv<D, false, false>();
+  if (e == cudaSuccess) e = set_bwd_kv<D, false, true>();
+  if (e == cudaSuccess) e = set_bwd_kv<D, true, false>();
+  if (e == cudaSuccess) e = set_bwd_kv<D, true, true>();
+  if (e == cudaSuccess) e = set_bwd_q<D, false, false, false>();
+  if (e == cudaSuccess) e = set_bwd_q<D, false, false, true>();
+  if (e == cudaSuccess) e = set_bwd_q<D, false, true, true>();
+  if (e == cudaSuccess) e = set_bwd_q<D, true, false, true>();
+  if (e == cudaSuccess) e = set_bwd_q<D, true, true, true>();
   return e;
 }
 

@@ -293,6 +293,25 @@ def test_every_cap_and_slopes_of_both_signs(cap):
             compare(run_backward(q, k, v, d_out, opts), ref, ("dq", "dk", "dv"))
 
 
+@pytest.mark.parametrize("cap", [0.0, 10.0, 500.0])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_one_visible_key_has_all_the_weight(dim, cap):
+    """A softmax over one key is exactly 1: out is v itself, and no score has a gradient."""
+    q, k, v, d_out = make(2, 70, 70, 4, 2, dim)
+    off = starts([[1] * 70])
+    opts = options(4, cap=cap, q_starts=off.expand(2, -1).contiguous(),
+                   kv_starts=off.expand(2, -1).contiguous())
+    got = run(q, k, v, opts)
+    assert torch.equal(got["out"].cpu(), v.repeat_interleave(2, dim=2))
+    grads = run_backward(q, k, v, d_out, opts)
+    # dP - delta is the same fp32 sum in two orders: dim terms of |dO v|, each order off by at
+    # most dim 2^-24 of their sum of magnitudes; the products with K or Q then scale it
+    dp = (d_out.double() * v.repeat_interleave(2, dim=2).double()).abs().sum(-1)
+    lim = 2 * dim * 2.0 ** -24 * float(dp.max()) * dim ** -0.5
+    assert float(grads["dq"].abs().max()) <= lim * float(k.abs().max()) * 1.01
+    assert float(grads["dk"].abs().max()) <= lim * 2 * float(q.abs().max()) * 1.01
+
+
 def test_strided_views_and_layouts():
     g = torch.Generator().manual_seed(4)
     qkv = torch.randn(2, 150, 8 + 2 * 2, 64, generator=g).bfloat16()
