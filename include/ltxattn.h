@@ -505,7 +505,7 @@ typedef struct ltxattn_masked_call {
  *   q_starts, kv_starts  not decreasing along a batch row, from 0 to q_len / kv_len.  They are
  *           read on the device; offsets that break this give unspecified values in out and
  *           lse, never an access outside the tensors.
- *   scale finite, > 0; softcap finite, >= 0; slopes finite
+ *   scale finite, > 0; softcap finite, >= 0, scale / softcap a normal fp32 number; slopes finite
  *   workspace  device, 16-byte aligned, at least what ltxattn_masked_workspace says.  Calls
  *           that may overlap in time (two streams, two captured graphs) need one each.
  * bf16 products, fp32 scores and statistics, P rounded to bf16 before the PV product, output

@@ -61,7 +61,7 @@ struct MaskedShape {
   float scale_log2;            // scale * log2(e)
   float cap_in;                // scale / cap
   float cap_log2;              // cap * log2(e)
-  float cap_poly[7];           // cap_log2 tanh(cap_in s) = s P(s^2) for |s| <= cap_limit
+  float cap_poly[6];           // cap_log2 tanh(z) = z P(z^2) for z = cap_in s, |s| <= cap_limit
   float cap_limit;
   const float* slopes;         // [heads] (kBias)
   int* status;
@@ -266,11 +266,11 @@ __device__ __forceinline__ bool cap_within(const float (&s)[N], const MaskedShap
 
 // The capped scores of two products within the polynomial's range.
 __device__ __forceinline__ float2 cap_pair(float2 x, const MaskedShape& p) {
-  const float2 y = __fmul2_rn(x, x);
-  float2 r = make_float2(p.cap_poly[6], p.cap_poly[6]);
+  const float2 z = __fmul2_rn(x, make_float2(p.cap_in, p.cap_in)), y = __fmul2_rn(z, z);
+  float2 r = make_float2(p.cap_poly[5], p.cap_poly[5]);
 #pragma unroll
-  for (int k = 5; k >= 0; --k) r = __ffma2_rn(r, y, make_float2(p.cap_poly[k], p.cap_poly[k]));
-  return __fmul2_rn(r, x);
+  for (int k = 4; k >= 0; --k) r = __ffma2_rn(r, y, make_float2(p.cap_poly[k], p.cap_poly[k]));
+  return __fmul2_rn(r, z);
 }
 
 // Turns a thread's N raw products into scores in log2 units when they are capped or biased;
@@ -278,11 +278,14 @@ __device__ __forceinline__ float2 cap_pair(float2 x, const MaskedShape& p) {
 //
 // The cap: tanh through the MUFU costs two of its operations per element ahead of the
 // softmax's own, three times what the products take.  While every product of the warp lies
-// within the cap (|scale q.k| <= cap: the usual case, as a cap is there for the outliers),
-// cap tanh(s / cap) is an odd polynomial of degree 13 in packed fused multiply-adds, with a
-// largest error of 1.0e-7 cap in fp32 (the coefficients are a least-squares fit of tanh on
-// [-1, 1], reweighted until its ripples are level).
-// Measured at 8192 x 8192 x 16 heads x 128: 755 us against 1229 us with tanh_ex2 alone.
+// within 0.8 of the cap (the usual case, as a cap is there for the outliers), cap tanh(s / cap)
+// is an odd polynomial of degree 11 in packed fused multiply-adds, with a largest error of
+// 1.0e-7 cap in fp32, as large as two more terms have on the whole of [-1, 1] (the coefficients
+// are a least-squares fit of tanh on [-0.8, 0.8], reweighted until its ripples are level).  The
+// argument is scaled first: folded into the coefficients the scale takes them below fp32's
+// range from a cap of 60 on.
+// Measured at 8192 x 8192 x 16 heads x 128, with a running maximum: 790 us against 1229 us with
+// tanh_ex2 alone.
 template <bool kCap, bool kBias, int N>
 __device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& p,
                                               float slope_log2, float far0, float dir) {
@@ -312,7 +315,7 @@ constexpr float kFixedMaxCap = 90.0f;
 // of O, and nothing that two threads would have to agree on before they use it.  So the two
 // softmax warpgroups share every tile, 64 keys each, instead of a tile each: a tile's softmax,
 // long because of the cap, takes half the time, and the tensor core has the other accumulator's
-// products to run meanwhile (8192 x 8192 x 16 heads x 128: 690 us; 790 us with a running maximum
+// products to run meanwhile (8192 x 8192 x 16 heads x 128: 730 us; 790 us with a running maximum
 // and a tile per warpgroup, 485 us without a cap).  A row's largest weight is then rounded to
 // bf16 like any other, where a running maximum makes it exactly 1: that shows in rows of few
 // keys, which are bound by latency anyway and keep the maximum (the host's rule).

@@ -99,8 +99,10 @@ int check_sizes(const ltxattn_masked_call& a) {
   if (!std::isfinite(a.scale) || !(a.scale > 0.0f) || !std::isfinite(a.softcap) ||
       a.softcap < 0.0f)
     return LTXATTN_ERR_INVALID_ARG;
-  // a cap so small that scale / cap overflows caps every score to +-cap: not a use
-  if (a.softcap > 0.0f && !std::isfinite(a.scale / a.softcap)) return LTXATTN_ERR_INVALID_ARG;
+  // scale / cap and cap log2(e) beyond fp32's normal range: not a use
+  if (!std::isfinite(a.scale * kLog2e) || !std::isfinite(a.softcap * kLog2e) ||
+      (a.softcap > 0.0f && !std::isnormal(a.scale / a.softcap)))
+    return LTXATTN_ERR_INVALID_ARG;
   if ((a.docs > 0) != (a.q_starts != nullptr) || (a.docs > 0) != (a.kv_starts != nullptr))
     return LTXATTN_ERR_INVALID_ARG;
   if (a.prefix && !a.causal) return LTXATTN_ERR_INVALID_ARG;
@@ -163,18 +165,12 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
   if (a.softcap > 0.0f) {
     s.cap_in = a.scale / a.softcap;
     s.cap_log2 = a.softcap * kLog2e;
-    // tanh(x) = x P(x^2) on [-1, 1], rescaled to take raw products; where a coefficient would
-    // leave the normal fp32 range the limit of 0 leaves every product to the general form
-    const double tanh_poly[7] = {0.9999997019767761, -0.33332130312919617,
-                                 0.13319583237171173, -0.053265832364559174,
-                                 0.019973276183009148, -0.005951274652034044,
-                                 0.0009637702605687082};
-    s.cap_limit = 1.0f / s.cap_in;
-    for (int i = 0; i < 7; ++i) {
-      const double c = tanh_poly[i] * (double)s.cap_log2 * std::pow((double)s.cap_in, 2 * i + 1);
-      s.cap_poly[i] = (float)c;
-      if (!(std::fabs(c) > 1e-37 && std::fabs(c) < 1e37)) s.cap_limit = 0.0f;
-    }
+    // tanh(z) = z P(z^2) on [-0.8, 0.8]
+    const double tanh_poly[6] = {0.9999996423721313,    -0.3333183228969574,
+                                 0.13313739001750946,   -0.052854713052511215,
+                                 0.018689367920160294, -0.004126554820686579};
+    s.cap_limit = 0.8f / s.cap_in;
+    for (int i = 0; i < 6; ++i) s.cap_poly[i] = (float)(tanh_poly[i] * s.cap_log2);
   }
   s.slopes = a.slopes;
   s.status = c.d_status;
@@ -186,7 +182,7 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
 // most of a row's weight: a running maximum with a cap, and dQ free of out's rounding without
 // one.  Their time is latency, not arithmetic (2 x 1003 keys, 12 heads of 64, causal: forward 42 us
 // with either form, backward 79 to 85 us with it and 75 to 86 us without); at 8192 keys the
-// maximum costs a capped forward call 790 us instead of 700, and the sum a plain backward a third.
+// maximum costs a capped forward call 790 us instead of 730, and the sum a plain backward a third.
 constexpr int kFewKeys = 2048;
 bool few_keys(const ltx::MaskedShape& s) { return s.kv_len / std::max(s.docs, 1) <= kFewKeys; }
 

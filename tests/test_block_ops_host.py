@@ -176,7 +176,8 @@ MASKED = [
     (dict(kv_len=0), INVALID), (dict(heads=0), INVALID), (dict(kv_heads=3), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(softcap=-1.0), INVALID), (dict(softcap=float("nan")), INVALID),
-    (dict(softcap=1e-44), INVALID), (dict(docs=-1), INVALID),
+    (dict(softcap=1e-44), INVALID), (dict(softcap=3e38), INVALID), (dict(scale=3e38), INVALID),
+    (dict(docs=-1), INVALID),
     (dict(docs=2), INVALID),                                   # no offsets
     (dict(q_starts=G, kv_starts=G + 256), INVALID),            # offsets of no document
     (dict(docs=2, q_starts=G), INVALID),

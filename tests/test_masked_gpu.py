@@ -293,6 +293,54 @@ def test_every_cap_and_slopes_of_both_signs(cap):
             compare(run_backward(q, k, v, d_out, opts), ref, ("dq", "dk", "dv"))
 
 
+@pytest.mark.parametrize("kv_len", [200, 5000])
+def test_caps_far_from_the_scores(kv_len):
+    """A huge cap changes nothing, a tiny one leaves the mean of v."""
+    q, k, v, d_out = make(1, 40, kv_len, 2, 2, 128)
+    q[:, 7:39] = 0
+    plain = run(q, k, v, options(2))["lse"]
+    # cap tanh(s / cap) is s (1 - s^2 / 3 cap^2); |s| < 9 in base 2 with a relative error of the
+    # polynomial (3e-7), its eight roundings and those of the plain product (2^-24 each)
+    huge = run(q, k, v, options(2, cap=1e6))["lse"]
+    assert float((huge - plain).abs().max()) <= 9 * (3e-7 + 12 * 2.0 ** -24)
+    opts = options(2, cap=1e-5)
+    tiny = run(q, k, v, opts)
+    # weights within e^(2 cap) of 1 / kv_len
+    assert float((tiny["lse"].cpu() - math.log2(kv_len)).abs().max()) <= 2e-5
+    mean = v.double().mean(1, keepdim=True)
+    far = (tiny["out"].cpu().double() - mean).abs()
+    # the result's rounding, P rounded to bf16 against a sum of it unrounded, 2 cap
+    lim = 2.0 ** -8 * mean.abs() + 2.0 ** -8 * v.double().abs().mean(1, keepdim=True)
+    assert torch.all(far <= lim + 2e-5 * 5)
+    assert all(torch.isfinite(t).all() for t in run_backward(q, k, v, d_out, opts).values())
+
+
+LONG = [
+    # rows of more keys than the form without a running maximum starts at, in both plans
+    (1, 150, 4200, 2, 2, 64, dict(causal=True, cap=30.0)),
+    (1, 2500, 2500, 4, 2, 128, dict(causal=True, cap=20.0, prefix=[[700]])),
+    (1, 300, 2300, 2, 1, 128, dict(cap=10.0, bias=True)),
+    (1, 2200, 2300, 2, 2, 64, dict(causal=True, cap=50.0, bias=True)),
+    (1, 700, 9000, 3, 3, 64, dict(cap=3.0, causal=True, q=[[200, 499]], kv=[[4000, 4990]])),
+    (2, 1, 9000, 8, 2, 128, dict(cap=5.0, bias=True)),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(str(x) for x in c))
+def test_long_capped_rows(case):
+    test_forward_matches_definition(case)
+    test_backward_matches_definition(case)
+
+
+@pytest.mark.parametrize("cap", [10.0, 62.0])
+def test_long_capped_rows_with_slopes_of_both_signs(cap):
+    for q_len, kv_len, causal in ((200, 2170, False), (2400, 2400, True)):
+        q, k, v, _ = make(1, q_len, kv_len, 4, 2, 64, seed=3)
+        opts = dict(softcap=cap, slopes=torch.tensor([0.5, 0.01, -0.02, -0.4]), causal=causal,
+                    scale=0.6)
+        compare(run(q, k, v, opts), block_ops.masked(q, k, v, **opts), ("out", "lse"))
+
+
 @pytest.mark.parametrize("cap", [0.0, 10.0, 500.0])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_one_visible_key_has_all_the_weight(dim, cap):
