@@ -219,9 +219,9 @@ struct MaskedSmem {
   static constexpr uint32_t kTmemCols = 512;
 };
 
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
   float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -257,11 +257,10 @@ __device__ __forceinline__ void masked_bias(float (&s)[N], const MaskedShape& p,
 // True when every product of the warp lies within the polynomial's range.  Whole warp.
 template <int N>
 __device__ __forceinline__ bool cap_within(const float (&s)[N], const MaskedShape& p) {
-  float lo = fmin3(s[0], s[1], s[2]);
+  float hi = max_abs3(s[0], s[1], s[2]);
 #pragma unroll
-  for (int c = 3; c + 1 < N; c += 2) lo = fmin3(lo, s[c], s[c + 1]);
-  lo = fminf(lo, s[N - 1]);
-  return !__any_sync(0xffffffffu, fmaxf(row_max<N>(s), -lo) > p.cap_limit);
+  for (int c = 3; c + 1 < N; c += 2) hi = max_abs3(hi, s[c], s[c + 1]);
+  return !__any_sync(0xffffffffu, max_abs3(hi, s[N - 1], s[N - 1]) > p.cap_limit);
 }
 
 // The capped scores of two products within the polynomial's range.

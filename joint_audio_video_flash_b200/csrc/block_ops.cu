@@ -334,14 +334,14 @@ int ltxattn_rope_axes(const ltxattn_rope_call* call, ltxattn_stream_t stream_) {
       (a.positions_batch != 1 && a.positions_batch != a.batch))
     return LTXATTN_ERR_INVALID_ARG;
   if (a.axes > ltx::kRopeMaxAxes) return LTXATTN_ERR_UNSUPPORTED;
-  int rotated = 0;
+  long long rotated = 0;
   for (int i = 0; i < a.axes; ++i) {
     if (a.axis_dims[i] < 0 || a.axis_dims[i] % 2 != 0 || a.axis_dims[i] > a.head_dim)
       return LTXATTN_ERR_INVALID_ARG;
     rotated += a.axis_dims[i];
   }
   if (rotated < 2 || rotated > a.head_dim) return LTXATTN_ERR_INVALID_ARG;
-  for (int i = 0; i < rotated / 2; ++i)
+  for (long long i = 0; i < rotated / 2; ++i)
     if (!std::isfinite(a.inv_freq[i])) return LTXATTN_ERR_INVALID_ARG;
   const bool halves = a.layout == LTXATTN_ROPE_HALVES;
   if (a.head_dim % (halves ? 16 : 8) != 0 || a.head_dim > 2 * ltx::kRopeMaxPairs ||
