@@ -61,8 +61,9 @@ struct MaskedShape {
   float scale_log2;            // scale * log2(e)
   float cap_in;                // scale / cap
   float cap_log2;              // cap * log2(e)
-  float cap_poly[6];           // cap_log2 tanh(z) = z P(z^2) for z = cap_in s, |s| <= cap_limit
-  float cap_limit;
+  // cap_log2 tanh(z) = z P(z^2) for z = cap_in s, |s| <= cap_limit[0] (6 terms), [1] (4 terms)
+  float cap_poly[6], cap_near[4];
+  float cap_limit[2];
   const float* slopes;         // [heads] (kBias)
   int* status;
   unsigned long long timeout_ns;
@@ -254,22 +255,43 @@ __device__ __forceinline__ void masked_bias(float (&s)[N], const MaskedShape& p,
   }
 }
 
-// True when every product of the warp lies within the polynomial's range.  Whole warp.
+// Terms of the polynomial that is exact enough for every product of the warp; 0: none is.
+// Whole warp.
 template <int N>
-__device__ __forceinline__ bool cap_within(const float (&s)[N], const MaskedShape& p) {
+__device__ __forceinline__ int cap_terms(const float (&s)[N], const MaskedShape& p) {
   float hi = max_abs3(s[0], s[1], s[2]);
 #pragma unroll
   for (int c = 3; c + 1 < N; c += 2) hi = max_abs3(hi, s[c], s[c + 1]);
-  return !__any_sync(0xffffffffu, max_abs3(hi, s[N - 1], s[N - 1]) > p.cap_limit);
+  hi = max_abs3(hi, s[N - 1], s[N - 1]);
+  if (!__any_sync(0xffffffffu, hi > p.cap_limit[1])) return 4;
+  return __any_sync(0xffffffffu, hi > p.cap_limit[0]) ? 0 : 6;
 }
 
 // The capped scores of two products within the polynomial's range.
+template <int kTerms>
 __device__ __forceinline__ float2 cap_pair(float2 x, const MaskedShape& p) {
+  const float(&k)[kTerms] = [&]() -> const float(&)[kTerms] {
+    if constexpr (kTerms == 4)
+      return p.cap_near;
+    else
+      return p.cap_poly;
+  }();
   const float2 z = __fmul2_rn(x, make_float2(p.cap_in, p.cap_in)), y = __fmul2_rn(z, z);
-  float2 r = make_float2(p.cap_poly[5], p.cap_poly[5]);
+  float2 r = make_float2(k[kTerms - 1], k[kTerms - 1]);
 #pragma unroll
-  for (int k = 4; k >= 0; --k) r = __ffma2_rn(r, y, make_float2(p.cap_poly[k], p.cap_poly[k]));
+  for (int i = kTerms - 2; i >= 0; --i) r = __ffma2_rn(r, y, make_float2(k[i], k[i]));
   return __fmul2_rn(r, z);
+}
+
+// Those of a thread's N products.
+template <int kTerms, int N>
+__device__ __forceinline__ void cap_all(float (&s)[N], const MaskedShape& p) {
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 r = cap_pair<kTerms>(make_float2(s[c], s[c + 1]), p);
+    s[c] = r.x;
+    s[c + 1] = r.y;
+  }
 }
 
 // Turns a thread's N raw products into scores in log2 units when they are capped or biased;
@@ -277,28 +299,25 @@ __device__ __forceinline__ float2 cap_pair(float2 x, const MaskedShape& p) {
 //
 // The cap: tanh through the MUFU costs two of its operations per element ahead of the
 // softmax's own, three times what the products take.  While every product of the warp lies
-// within 0.8 of the cap (the usual case, as a cap is there for the outliers), cap tanh(s / cap)
-// is an odd polynomial of degree 11 in packed fused multiply-adds, with a largest error of
-// 1.0e-7 cap in fp32, as large as two more terms have on the whole of [-1, 1] (the coefficients
-// are a least-squares fit of tanh on [-0.8, 0.8], reweighted until its ripples are level).  The
-// argument is scaled first: folded into the coefficients the scale takes them below fp32's
-// range from a cap of 60 on.
-// Measured at 8192 x 8192 x 16 heads x 128, with a running maximum: 790 us against 1229 us with
-// tanh_ex2 alone.
+// within 0.8 of the cap, cap tanh(s / cap) is an odd polynomial of degree 11 in packed fused
+// multiply-adds, within 0.4 of the cap (the usual case, as a cap is there for the outliers) one
+// of degree 7; either is off by 1.0e-7 cap at most in fp32 (the coefficients are least-squares
+// fits of tanh on these ranges, reweighted until the ripples are level).  The argument is scaled
+// first: folded into the coefficients the scale takes them below fp32's range from a cap of 60
+// on.  Measured at 8192 x 8192 x 16 heads x 128, N(0, 1) scores, with a running maximum: 1229 us
+// with tanh_ex2 alone, 800 us with degree 11 alone, 720 us.
 template <bool kCap, bool kBias, int N>
 __device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& p,
                                               float slope_log2, float far0, float dir) {
   if constexpr (kCap) {
-    if (!cap_within(s, p)) {
-#pragma unroll
-      for (int c = 0; c < N; ++c) s[c] = tanh_ex2(s[c] * p.cap_in) * p.cap_log2;
+    const int terms = cap_terms(s, p);
+    if (terms == 4) {
+      cap_all<4>(s, p);
+    } else if (terms == 6) {
+      cap_all<6>(s, p);
     } else {
 #pragma unroll
-      for (int c = 0; c < N; c += 2) {
-        const float2 r = cap_pair(make_float2(s[c], s[c + 1]), p);
-        s[c] = r.x;
-        s[c + 1] = r.y;
-      }
+      for (int c = 0; c < N; ++c) s[c] = tanh_ex2(s[c] * p.cap_in) * p.cap_log2;
     }
   }
   if constexpr (kBias) masked_bias<kCap>(s, p, slope_log2, far0, dir);
@@ -314,7 +333,7 @@ constexpr float kFixedMaxCap = 90.0f;
 // of O, and nothing that two threads would have to agree on before they use it.  So the two
 // softmax warpgroups share every tile, 64 keys each, instead of a tile each: a tile's softmax,
 // long because of the cap, takes half the time, and the tensor core has the other accumulator's
-// products to run meanwhile (8192 x 8192 x 16 heads x 128: 730 us; 790 us with a running maximum
+// products to run meanwhile (8192 x 8192 x 16 heads x 128: 680 us; 720 us with a running maximum
 // and a tile per warpgroup, 485 us without a cap).  A row's largest weight is then rounded to
 // bf16 like any other, where a running maximum makes it exactly 1: that shows in rows of few
 // keys, which are bound by latency anyway and keep the maximum (the host's rule).
@@ -629,8 +648,13 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
                 pk[x] = pack_bf16x2(e.x, e.y);
               }
             };
-            if (!kBias && !masked && cap_within(v, p.s)) {
-              weights([&](int x) { return cap_pair(make_float2(v[2 * x], v[2 * x + 1]), p.s); });
+            const int terms = kBias || masked ? 0 : cap_terms(v, p.s);
+            if (terms == 4) {
+              weights(
+                  [&](int x) { return cap_pair<4>(make_float2(v[2 * x], v[2 * x + 1]), p.s); });
+            } else if (terms == 6) {
+              weights(
+                  [&](int x) { return cap_pair<6>(make_float2(v[2 * x], v[2 * x + 1]), p.s); });
             } else {
               masked_scores<kCap, kBias>(v, p.s, slope, (float)(place_a - c0), -1.0f);
               if (masked) {

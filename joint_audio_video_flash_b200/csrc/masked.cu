@@ -165,12 +165,16 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
   if (a.softcap > 0.0f) {
     s.cap_in = a.scale / a.softcap;
     s.cap_log2 = a.softcap * kLog2e;
-    // tanh(z) = z P(z^2) on [-0.8, 0.8]
+    // tanh(z) = z P(z^2) on [-0.8, 0.8] and on [-0.4, 0.4]
     const double tanh_poly[6] = {0.9999996423721313,    -0.3333183228969574,
                                  0.13313739001750946,   -0.052854713052511215,
                                  0.018689367920160294, -0.004126554820686579};
-    s.cap_limit = 0.8f / s.cap_in;
+    const double tanh_near[4] = {0.9999995827674866, -0.3332972526550293, 0.13250567018985748,
+                                 -0.04682572931051254};
+    s.cap_limit[0] = 0.8f / s.cap_in;
+    s.cap_limit[1] = 0.4f / s.cap_in;
     for (int i = 0; i < 6; ++i) s.cap_poly[i] = (float)(tanh_poly[i] * s.cap_log2);
+    for (int i = 0; i < 4; ++i) s.cap_near[i] = (float)(tanh_near[i] * s.cap_log2);
   }
   s.slopes = a.slopes;
   s.status = c.d_status;
@@ -182,7 +186,7 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
 // most of a row's weight: a running maximum with a cap, and dQ free of out's rounding without
 // one.  Their time is latency, not arithmetic (2 x 1003 keys, 12 heads of 64, causal: forward 42 us
 // with either form, backward 79 to 85 us with it and 75 to 86 us without); at 8192 keys the
-// maximum costs a capped forward call 790 us instead of 730, and the sum a plain backward a third.
+// maximum costs a capped forward call 720 us instead of 680, and the sum a plain backward a third.
 constexpr int kFewKeys = 2048;
 bool few_keys(const ltx::MaskedShape& s) { return s.kv_len / std::max(s.docs, 1) <= kFewKeys; }
 
