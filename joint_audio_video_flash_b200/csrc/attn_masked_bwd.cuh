@@ -37,11 +37,13 @@
 // shared memory.  Rows of Q, dO (kv) or K, V (q) behind the document are set to zero in shared
 // memory: they are B operands, and 0 times whatever follows in memory has to be 0.
 //
-// P and dS are rounded to bf16 for their products; everything else is fp32 until the one
-// rounding of each gradient.
+// P and dS are rounded to bf16 for their products; with kFine (short walks, the host's rule) what
+// that takes off is rounded too and multiplied as a second operand, 16 bits of each in all.
+// Everything else is fp32 until the one rounding of each gradient.
 #pragma once
 
 #include <climits>
+#include <type_traits>
 
 #include "attn_masked_fwd.cuh"
 
@@ -82,6 +84,29 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int live) {
       *reinterpret_cast<uint4*>(tile + bx * kBoxBytes + o) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// Writes 32 of a warp's P or dS values a row over the 32 columns they came from, as bf16: with
+// kFine what the rounding took off follows in the columns that are left, to be multiplied too.
+template <bool kFine>
+__device__ __forceinline__ void store_operand(uint32_t col, const float (&v)[32]) {
+  uint32_t hi[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) hi[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+  tmem_st16(col, hi);
+  if constexpr (kFine) {
+    uint32_t lo[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      lo[x] = pack_bf16x2(v[2 * x] - __uint_as_float(hi[x] << 16),
+                          v[2 * x + 1] - __uint_as_float(hi[x] & 0xffff0000u));
+    tmem_st16(col + 16, lo);
+  }
+}
+
+// Column of the kk-th 16 keys (or queries) of such an operand, written 32 at a time.
+__device__ __forceinline__ constexpr uint32_t operand_col(int kk) {
+  return (kk >> 1) * 32 + (kk & 1) * 8;
 }
 
 // Writes 128 rows of D fp32 accumulator columns, times `scale`: bf16 rows through the staging
@@ -185,7 +210,7 @@ struct BwdKvSmem {
   static constexpr uint32_t kTmemCols = 512;
 };
 
-template <int D, bool kCap, bool kBias>
+template <int D, bool kCap, bool kBias, bool kFine>
 __global__ void __launch_bounds__(kMaskedThreads, 1)
     ltx_masked_bwd_kv(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -349,9 +374,11 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ts_elect(tmem + acc, tmem + col + g * 64 + kk * 8,
-                          bd.at(off_b + (g * 4 + kk) * 16 * 128), idesc_d,
-                          (t > 0 || g > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+            for (int y = 0; y < (kFine ? 2 : 1); ++y)
+              umma_ts_elect(tmem + acc, tmem + col + g * 64 + operand_col(kk) + y * 16,
+                            bd.at(off_b + (g * 4 + kk) * 16 * 128), idesc_d,
+                            (t > 0 || g > 0 || kk > 0 || y > 0) ? 1u : 0u);
         }
         return true;
       };
@@ -479,24 +506,21 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint32_t pk[16];
+        float w[32];
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
           const float4 l4 = *reinterpret_cast<const float4*>(mine + c * 32 + x);
           const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-          float e[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int q = c * 32 + x + y;
             float a = kCap || kBias ? s[q] - l[y] : fmaf(s[q], p.s.scale_log2, -l[y]);
             if (masked && i0 + q < from) a = -INFINITY;
-            e[y] = ex2(a);
-            s[q] = kCap ? e[y] * bent[q] : e[y];
+            w[x + y] = ex2(a);
+            s[q] = kCap ? w[x + y] * bent[q] : w[x + y];
           }
-          pk[x / 2] = pack_bf16x2(e[0], e[1]);
-          pk[x / 2 + 1] = pack_bf16x2(e[2], e[3]);
         }
-        tmem_st16(trow + L::kColS + g * 64 + c * 16, pk);
+        store_operand<kFine>(trow + L::kColS + g * 64 + c * 32, w);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -511,16 +535,15 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         float d[32];
         tmem_ld32(trow + L::kColDp + g * 64 + c * 32, d);
         tmem_ld_wait();
-        uint32_t pk[16];
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
           const float4 e = *reinterpret_cast<const float4*>(mine + 64 + c * 32 + x);
-          pk[x / 2] = pack_bf16x2(s[c * 32 + x] * (d[x] - e.x),
-                                  s[c * 32 + x + 1] * (d[x + 1] - e.y));
-          pk[x / 2 + 1] = pack_bf16x2(s[c * 32 + x + 2] * (d[x + 2] - e.z),
-                                      s[c * 32 + x + 3] * (d[x + 3] - e.w));
+          d[x] = s[c * 32 + x] * (d[x] - e.x);
+          d[x + 1] = s[c * 32 + x + 1] * (d[x + 1] - e.y);
+          d[x + 2] = s[c * 32 + x + 2] * (d[x + 2] - e.z);
+          d[x + 3] = s[c * 32 + x + 3] * (d[x + 3] - e.w);
         }
-        tmem_st16(trow + L::kColDp + g * 64 + c * 16, pk);
+        store_operand<kFine>(trow + L::kColDp + g * 64 + c * 32, d);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -600,13 +623,14 @@ struct BwdQSmem {
   static constexpr uint32_t kTmemCols = 512;
 };
 
-template <int D, bool kCap, bool kBias, bool kFix>
+template <int D, bool kCap, bool kBias, bool kFix, bool kFine>
 __global__ void __launch_bounds__(kMaskedThreads, 1)
     ltx_masked_bwd_q(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ MaskedBwdParams p) {
+  static_assert(kFix || !kFine, "exact products leave out's rounding as the largest error");
   using L = BwdQSmem<D, kFix>;
   constexpr int kSBuf = L::kSBuf;
   extern __shared__ uint8_t smem_raw[];
@@ -771,7 +795,8 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         return true;
       };
       // acc (+)= A K_t, A the 128 x 128 bf16 operand at `col` (the halves at +0 and +64)
-      auto gather = [&](uint32_t acc, uint32_t col, int ready, int t) -> bool {
+      auto gather = [&](uint32_t acc, uint32_t col, int ready, int t, auto fine_) -> bool {
+        constexpr bool fine = decltype(fine_)::value;
         const uint32_t off = (uint32_t)(t % L::kKStages) * L::kTileBytes;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -779,9 +804,11 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ts_elect(tmem + acc, tmem + col + g * 64 + kk * 8,
-                          dk_t.at(off + (g * 4 + kk) * 16 * 128), idesc_d,
-                          (t > 0 || g > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+            for (int y = 0; y < (fine ? 2 : 1); ++y)
+              umma_ts_elect(tmem + acc, tmem + col + g * 64 + operand_col(kk) + y * 16,
+                            dk_t.at(off + (g * 4 + kk) * 16 * 128), idesc_d,
+                            (t > 0 || g > 0 || kk > 0 || y > 0) ? 1u : 0u);
         }
         return true;
       };
@@ -789,11 +816,11 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       if (ok && !kFix && n > 1) ok = s_of(1);
       for (int t = 0; t < n && ok; ++t) {
         if constexpr (kFix) {
-          ok = gather(L::kColPk, L::kColS, L::bP, t);
+          ok = gather(L::kColPk, L::kColS, L::bP, t, std::false_type{});
           if (ok && t + 1 < n) ok = s_of(t + 1);
           if (!ok) break;
         }
-        ok = gather(L::kColQ, L::kColDp, L::bDs, t);
+        ok = gather(L::kColQ, L::kColDp, L::bDs, t, std::bool_constant<kFine>{});
         if (!ok) break;
         umma_commit_elect(bar(L::bKE + t % L::kKStages));
         if (t + 1 < n) ok = dp_of(t + 1);
@@ -885,13 +912,10 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       if constexpr (kFix) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
+          float w[32];
 #pragma unroll
-          for (int x = 0; x < 16; ++x)
-            pk[x] = kCap ? pack_bf16x2(s[c * 32 + 2 * x] * bent[c * 32 + 2 * x],
-                                       s[c * 32 + 2 * x + 1] * bent[c * 32 + 2 * x + 1])
-                         : pack_bf16x2(s[c * 32 + 2 * x], s[c * 32 + 2 * x + 1]);
-          tmem_st16(trow + L::kColS + g * 64 + c * 16, pk);
+          for (int x = 0; x < 32; ++x) w[x] = kCap ? s[c * 32 + x] * bent[c * 32 + x] : s[c * 32 + x];
+          store_operand<false>(trow + L::kColS + g * 64 + c * 32, w);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -906,7 +930,6 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         float d[32];
         tmem_ld32(trow + L::kColDp + g * 64 + c * 32, d);
         tmem_ld_wait();
-        uint32_t pk[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const int q = c * 32 + 2 * x;
@@ -914,9 +937,10 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
                                       __fadd2_rn(make_float2(d[2 * x], d[2 * x + 1]),
                                                  make_float2(-st.y, -st.y)));
           off2 = __fadd2_rn(off2, r);
-          pk[x] = kCap ? pack_bf16x2(r.x * bent[q], r.y * bent[q + 1]) : pack_bf16x2(r.x, r.y);
+          d[2 * x] = kCap ? r.x * bent[q] : r.x;
+          d[2 * x + 1] = kCap ? r.y * bent[q + 1] : r.y;
         }
-        tmem_st16(trow + L::kColDp + g * 64 + c * 16, pk);
+        store_operand<kFine>(trow + L::kColDp + g * 64 + c * 32, d);
       }
       tmem_st_wait();
       tc_fence_before();

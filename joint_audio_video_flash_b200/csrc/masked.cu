@@ -191,6 +191,17 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
 constexpr int kFewKeys = 2048;
 bool few_keys(const ltx::MaskedShape& s) { return s.kv_len / std::max(s.docs, 1) <= kFewKeys; }
 
+// Where a document's queries or keys are one tile (on average), sums have too few terms for the
+// roundings of P and dS to average out, and the backward kernels multiply what the roundings take
+// off as well: relative to the gradients' norm, 2.9e-3 becomes 1.7e-3 (the result's own rounding)
+// at 16 x 16 tokens, for 10 to 15 % of time that is mostly latency (2 x 126 x 15360 x 32 x 64: 404
+// us without, 470 us with it; 2 x 252 in documents of 124: 18.6 us and 20.4 us).  Longer walks
+// would pay 6 products instead of 4 and have 2.4e-3 anyway.
+constexpr int kFineRows = 128;
+bool fine(const ltx::MaskedShape& s) {
+  return std::min(s.q_len, s.kv_len) / std::max(s.docs, 1) <= kFineRows;
+}
+
 long long grid_ctas(int units, int heads, int batch, int parts) {
   return (long long)units * heads * batch * parts;
 }
@@ -280,7 +291,7 @@ template <int D, bool kAlt>
 cudaError_t launch_fwd_scores(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const ltx::MaskedFwdParams& p, int units,
                               cudaStream_t stream) {
-  if (cap && p.s.cap_log2 <= ltx::kFixedMaxCap && !few_keys(p.s))
+  if (cap && p.s.cap_log2 <= ltx::kFixedMaxCap && !few_keys(p.s) && !fine(p.s))
     return bias ? launch_fwd<D, kAlt, true, true, true>(tq, tk, tv, p, units, stream)
                 : launch_fwd<D, kAlt, true, false, true>(tq, tk, tv, p, units, stream);
   if (cap)
@@ -314,8 +325,8 @@ struct BwdPlan {
 };
 
 // Whether the dQ kernel carries the sum that takes out's rounding off dQ (attn_masked_bwd.cuh):
-// where scores are capped or biased, or rows have few keys.
-bool dq_fix(const ltx::MaskedShape& s, bool cap) { return cap || s.slopes || few_keys(s); }
+// where scores are capped or biased, or rows have few keys, or P and dS are exact.
+bool dq_fix(const ltx::MaskedShape& s, bool cap) { return cap || s.slopes || fine(s) || few_keys(s); }
 
 BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, bool cap, int num_sms) {
   BwdPlan f;
@@ -344,22 +355,45 @@ struct BwdMaps {
   CUtensorMap q, k, v, d_out;
 };
 
-template <int D, bool kCap, bool kBias>
+template <int D, bool kCap, bool kBias, bool kFine>
 cudaError_t launch_kv(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
                       cudaStream_t stream) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.kv_heads, p.s.batch, p.parts);
-  return ltx::launch_dependent(ltx::ltx_masked_bwd_kv<D, kCap, kBias>, grid, ltx::kMaskedThreads,
-                               ltx::BwdKvSmem<D>::kAlloc, stream, t.q, t.k, t.v, t.d_out, p);
+  return ltx::launch_dependent(ltx::ltx_masked_bwd_kv<D, kCap, kBias, kFine>, grid,
+                               ltx::kMaskedThreads, ltx::BwdKvSmem<D>::kAlloc, stream, t.q, t.k,
+                               t.v, t.d_out, p);
 }
 
-template <int D, bool kCap, bool kBias, bool kFix>
+template <int D, bool kCap, bool kBias, bool kFix, bool kFine>
 cudaError_t launch_q(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
                      cudaStream_t stream) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.heads, p.s.batch, p.parts);
-  ltx::ltx_masked_bwd_q<D, kCap, kBias, kFix>
+  ltx::ltx_masked_bwd_q<D, kCap, kBias, kFix, kFine>
       <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D, kFix>::kAlloc, stream>>>(t.q, t.k, t.v,
                                                                               t.d_out, p);
   return cudaGetLastError();
+}
+
+template <int D, bool kCap, bool kBias>
+cudaError_t launch_both(bool of_q, bool fine, bool fix, const BwdMaps& t,
+                        const ltx::MaskedBwdParams& p, int units, cudaStream_t stream) {
+  if (!of_q)
+    return fine ? launch_kv<D, kCap, kBias, true>(t, p, units, stream)
+                : launch_kv<D, kCap, kBias, false>(t, p, units, stream);
+  if (fine) return launch_q<D, kCap, kBias, true, true>(t, p, units, stream);
+  if constexpr (!kCap && !kBias)
+    if (!fix) return launch_q<D, false, false, false, false>(t, p, units, stream);
+  return launch_q<D, kCap, kBias, true, false>(t, p, units, stream);
+}
+
+template <int D>
+cudaError_t launch_scores(bool of_q, bool cap, bool fine, bool fix, const BwdMaps& t,
+                          const ltx::MaskedBwdParams& p, int units, cudaStream_t stream) {
+  const bool bias = p.s.slopes != nullptr;
+  return cap ? (bias ? launch_both<D, true, true>(of_q, fine, fix, t, p, units, stream)
+                     : launch_both<D, true, false>(of_q, fine, fix, t, p, units, stream))
+             : (bias ? launch_both<D, false, true>(of_q, fine, fix, t, p, units, stream)
+                     : launch_both<D, false, false>(of_q, fine, fix, t, p, units, stream));
 }
 
 template <int D, bool kDq>
@@ -390,7 +424,7 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
   set_target(d_out, &base, p.d_out_stride);
   p.d_out = base;
   p.lse = a.lse;
-  const bool cap = a.softcap > 0.0f, bias = a.slopes != nullptr, fix = dq_fix(p.s, cap);
+  const bool cap = a.softcap > 0.0f, fix = dq_fix(p.s, cap);
   // dQ first: it leaves delta free of out's rounding
   p.parts = f.parts_q;
   set_target(dq, &p.d0, p.stride0);
@@ -400,12 +434,7 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
     p.part1 = fix ? partials + rows * D : nullptr;
     p.part_e = partials + rows * D * (fix ? 2 : 1);
   }
-  cudaError_t e =
-      cap ? (bias ? launch_q<D, true, true, true>(maps, p, f.units_q, stream)
-                  : launch_q<D, true, false, true>(maps, p, f.units_q, stream))
-          : (bias  ? launch_q<D, false, true, true>(maps, p, f.units_q, stream)
-             : fix ? launch_q<D, false, false, true>(maps, p, f.units_q, stream)
-                   : launch_q<D, false, false, false>(maps, p, f.units_q, stream));
+  cudaError_t e = launch_scores<D>(true, cap, fine(p.s), fix, maps, p, f.units_q, stream);
   if (e == cudaSuccess && p.parts > 1)
     e = launch_sum<D, true>(p, stream);
   if (e != cudaSuccess) return e;
@@ -418,39 +447,35 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
     p.part0 = partials;
     p.part1 = partials + (size_t)p.parts * a.batch * a.kv_heads * a.kv_len * D;
   }
-  e = cap ? (bias ? launch_kv<D, true, true>(maps, p, f.units_kv, stream)
-                  : launch_kv<D, true, false>(maps, p, f.units_kv, stream))
-          : (bias ? launch_kv<D, false, true>(maps, p, f.units_kv, stream)
-                  : launch_kv<D, false, false>(maps, p, f.units_kv, stream));
+  e = launch_scores<D>(false, cap, fine(p.s), fix, maps, p, f.units_kv, stream);
   if (e == cudaSuccess && p.parts > 1) e = launch_sum<D, false>(p, stream);
   return e;
 }
 
-template <int D, bool kCap, bool kBias>
-cudaError_t set_bwd_kv() {
-  return cudaFuncSetAttribute(ltx::ltx_masked_bwd_kv<D, kCap, kBias>,
+template <int D, bool kCap, bool kBias, bool kFine>
+cudaError_t set_bwd() {
+  cudaError_t e = cudaFuncSetAttribute(ltx::ltx_masked_bwd_kv<D, kCap, kBias, kFine>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       ltx::BwdKvSmem<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, kCap, kBias, true, kFine>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ltx::BwdKvSmem<D>::kAlloc);
-}
-
-template <int D, bool kCap, bool kBias, bool kFix>
-cudaError_t set_bwd_q() {
-  return cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, kCap, kBias, kFix>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ltx::BwdQSmem<D, kFix>::kAlloc);
+                              ltx::BwdQSmem<D, true>::kAlloc);
 }
 
 template <int D>
 cudaError_t set_bwd_scores() {
-  cudaError_t e = set_bwd_kv<D, false, false>();
-  if (e == cudaSuccess) e = set_bwd_kv<D, false, true>();
-  if (e == cudaSuccess) e = set_bwd_kv<D, true, false>();
-  if (e == cudaSuccess) e = set_bwd_kv<D, true, true>();
-  if (e == cudaSuccess) e = set_bwd_q<D, false, false, false>();
-  if (e == cudaSuccess) e = set_bwd_q<D, false, false, true>();
-  if (e == cudaSuccess) e = set_bwd_q<D, false, true, true>();
-  if (e == cudaSuccess) e = set_bwd_q<D, true, false, true>();
-  if (e == cudaSuccess) e = set_bwd_q<D, true, true, true>();
+  cudaError_t e = cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, false, false, false, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       ltx::BwdQSmem<D, false>::kAlloc);
+  if (e == cudaSuccess) e = set_bwd<D, false, false, false>();
+  if (e == cudaSuccess) e = set_bwd<D, false, false, true>();
+  if (e == cudaSuccess) e = set_bwd<D, false, true, false>();
+  if (e == cudaSuccess) e = set_bwd<D, false, true, true>();
+  if (e == cudaSuccess) e = set_bwd<D, true, false, false>();
+  if (e == cudaSuccess) e = set_bwd<D, true, false, true>();
+  if (e == cudaSuccess) e = set_bwd<D, true, true, false>();
+  if (e == cudaSuccess) e = set_bwd<D, true, true, true>();
   return e;
 }
 
