@@ -544,7 +544,8 @@ typedef struct ltxattn_masked_grad {
  *
  *   workspace  device, 16-byte aligned, at least what ltxattn_masked_workspace(call, 1) says;
  *              calls that may overlap in time need one each.
- * bf16 products with P and dS rounded to bf16 ahead of theirs, everything else fp32, each
+ * bf16 products with P and dS rounded to bf16 ahead of theirs (to 16 bits, as two products,
+ * where documents have 128 queries or keys or fewer on average), everything else fp32, each
  * gradient rounded once.  Sums run in a fixed order (the same call gives the same bits).
  * Needs ltxattn_create; checks and errors as ltxattn_masked_forward.
  */
