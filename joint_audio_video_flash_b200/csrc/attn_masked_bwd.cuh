@@ -233,11 +233,15 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
   const int hk = at_work.head, b = at_work.b, part = at_work.part;
 
   grid_dependency_wait();
-  if (warp == 2) {
+  // one barrier ahead of the work: what each warp prepares does not need the others
+  if (warp == 1) {
+    tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
+    tmem_relinquish();
+  } else if (warp == 2) {
     const MaskedDoc m = masked_find<true>(p.s, b, at_work.unit, kBlockN);
     if (lane == 0) *shared_doc = m;
-  }
-  if (threadIdx.x == 0) {
+  } else if (threadIdx.x == 0) {
+    const int status = *reinterpret_cast<volatile int*>(p.s.status);
     mbar_init(bar(L::bKF), 1);
     mbar_init(bar(L::bVF), 1);
     for (int s = 0; s < L::kStages; ++s) {
@@ -254,21 +258,23 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     }
     mbar_init(bar(L::bEnd), 1);
     mbar_init(bar(L::bDrain), 1);
-    *abort_flag = (*reinterpret_cast<volatile int*>(p.s.status) != kDevOk) ? 1 : 0;
     fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+    *abort_flag = status != kDevOk ? 1 : 0;
   }
   grid_dependents_launch();
-  __syncthreads();
-  const MaskedDoc m = *shared_doc;
-  if (m.tile < 0) return;
-  if (warp == 1) {
-    tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const MaskedDoc m = *shared_doc;
   const uint32_t tmem = *tmem_slot;
+  if (m.tile < 0) {
+    if (warp == 1) tmem_dealloc(tmem, L::kTmemCols);
+    return;
+  }
   const WaitCtl ctl{abort_flag, p.s.status, p.s.timeout_ns};
 
   // the query tiles that see a key of this tile: from tile `qt0` on; the walk goes over them
@@ -287,10 +293,6 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     setmaxnreg_dec<kMaskedRegsProducer>();
     if (warp == 0 && lane == 0 && n > 0 && !*abort_flag) {
       // ---------------------------------------------------------- TMA producer
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-      tma_prefetch_desc(&tm_do);
       mbar_arrive_expect_tx(bar(L::bKF), L::kTileBytes);
       for (int bx = 0; bx < L::kBoxes; ++bx)
         tma_load_4d(sbase + L::kK + bx * L::kBoxBytes, &tm_k, bar(L::bKF), bx * 64, hk,
@@ -648,11 +650,15 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
   const int h = at_work.head, b = at_work.b, part = at_work.part;
   const int hk = h / p.s.group;
 
-  if (warp == 2) {
+  // one barrier ahead of the work: what each warp prepares does not need the others
+  if (warp == 1) {
+    tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
+    tmem_relinquish();
+  } else if (warp == 2) {
     const MaskedDoc m = masked_find<false>(p.s, b, at_work.unit, kBlockM);
     if (lane == 0) *shared_doc = m;
-  }
-  if (threadIdx.x == 0) {
+  } else if (threadIdx.x == 0) {
+    const int status = *reinterpret_cast<volatile int*>(p.s.status);
     mbar_init(bar(L::bQF), 1);
     mbar_init(bar(L::bOF), 1);
     for (int s = 0; s < L::kKStages; ++s) {
@@ -671,21 +677,23 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     mbar_init(bar(L::bDp), 1);
     mbar_init(bar(L::bEnd), 1);
     mbar_init(bar(L::bDrain), 1);
-    *abort_flag = (*reinterpret_cast<volatile int*>(p.s.status) != kDevOk) ? 1 : 0;
     fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+    *abort_flag = status != kDevOk ? 1 : 0;
   }
   grid_dependents_launch();
-  __syncthreads();
-  const MaskedDoc m = *shared_doc;
-  if (m.tile < 0) return;
-  if (warp == 1) {
-    tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const MaskedDoc m = *shared_doc;
   const uint32_t tmem = *tmem_slot;
+  if (m.tile < 0) {
+    if (warp == 1) tmem_dealloc(tmem, L::kTmemCols);
+    return;
+  }
   const WaitCtl ctl{abort_flag, p.s.status, p.s.timeout_ns};
 
   const int i0 = m.tile * kBlockM;
@@ -699,10 +707,6 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     setmaxnreg_dec<kMaskedRegsProducer>();
     if (warp == 0 && lane == 0 && n > 0 && !*abort_flag) {
       // ---------------------------------------------------------- TMA producer
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-      tma_prefetch_desc(&tm_do);
       mbar_arrive_expect_tx(bar(L::bQF), L::kTileBytes);
       for (int bx = 0; bx < L::kBoxes; ++bx)
         tma_load_4d(sbase + L::kQ + bx * L::kBoxBytes, &tm_q, bar(L::bQF), bx * 64, h,

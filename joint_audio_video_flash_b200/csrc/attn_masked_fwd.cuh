@@ -53,6 +53,7 @@ struct MaskedShape {
   int batch, q_len, kv_len;
   int heads, kv_heads, group;  // group = heads / kv_heads
   int pack;                    // query heads packed into a tile's rows (1 = none)
+  int pack_bits;               // log2 of it: integer divisions cost more than a tile's row
   int docs;                    // documents per batch row; 0 = one, without offsets
   const int* q_starts;         // [batch][docs + 1]
   const int* kv_starts;
@@ -358,19 +359,23 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int pack = p.s.pack;
-  const MaskedPlace at_work = masked_place(p.s.heads / pack, p.s.batch, p.parts);
+  const MaskedPlace at_work = masked_place(p.s.heads >> p.s.pack_bits, p.s.batch, p.parts);
   const int hy = at_work.head;  // key head when heads are packed, else query head
   const int b = at_work.b, part = at_work.part;
-  const int tile_tokens = kBlockM / pack;
+  const int tile_tokens = kBlockM >> p.s.pack_bits;
   const int h0 = hy * pack;                            // first query head of the rows
   const int hk = pack > 1 ? hy : hy / p.s.group;       // key head
 
-  if (warp == 2) {
+  // one barrier ahead of the work: what each warp prepares does not need the others
+  if (warp == 1) {
+    tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
+    tmem_relinquish();
+  } else if (warp == 2) {
     const MaskedDoc m =
         masked_find<false>(p.s, b, at_work.unit, tile_tokens * L::kQTiles);
     if (lane == 0) *shared_doc = m;
-  }
-  if (threadIdx.x == 0) {
+  } else if (threadIdx.x == 0) {
+    const int status = *reinterpret_cast<volatile int*>(p.s.status);
     for (int g = 0; g < 2; ++g) {
       mbar_init(bar(L::bQF + g), 1);
       mbar_init(bar(L::bSF + g), 1);
@@ -385,21 +390,22 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       mbar_init(bar(L::bVE + s), 1);
     }
     mbar_init(bar(L::bDrain), 1);
-    *abort_flag = (*reinterpret_cast<volatile int*>(p.s.status) != kDevOk) ? 1 : 0;
     fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    *abort_flag = status != kDevOk ? 1 : 0;
   }
   grid_dependents_launch();
-  __syncthreads();
-  const MaskedDoc m = *shared_doc;
-  if (m.tile < 0) return;  // fewer units than the host's bound; nothing was allocated yet
-  if (warp == 1) {
-    tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const MaskedDoc m = *shared_doc;
   const uint32_t tmem = *tmem_slot;
+  if (m.tile < 0) {  // fewer units than the host's bound
+    if (warp == 1) tmem_dealloc(tmem, L::kTmemCols);
+    return;
+  }
   const WaitCtl ctl{abort_flag, p.s.status, p.s.timeout_ns};
 
   // first token of each query tile, key tiles each sees, and this CTA's part of them
@@ -426,9 +432,6 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     setmaxnreg_dec<kMaskedRegsProducer>();
     if (warp == 0 && lane == 0 && n > 0 && !*abort_flag) {
       // ---------------------------------------------------------- TMA producer
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
       const bool second = !kAlt && n1 > 0;
       for (int g = 0; g < (second ? 2 : 1); ++g) {
         mbar_arrive_expect_tx(bar(L::bQF + g), L::kTileBytes);
@@ -569,15 +572,15 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     const uint32_t colS = L::kColS + 128 * g;
     const uint32_t colO = L::kColO + D * g;
     const int tile0 = tok0 + (kAlt ? 0 : g * tile_tokens);
-    const int i = tile0 + row / pack;  // query of the document
-    const int h = h0 + row % pack;
+    const int i = tile0 + (row >> p.s.pack_bits);  // query of the document
+    const int h = h0 + (row & (pack - 1));
     const bool valid = i < m.nq;
     // a warp without a query row only keeps the barriers moving: its rows of S, P and O hold
     // whatever they hold, and no other row depends on them
-    const bool live_warp = tile0 + (wq * 32) / pack < m.nq;
+    const bool live_warp = tile0 + ((wq * 32) >> p.s.pack_bits) < m.nq;
     const int lim = masked_limit(m, p.s.causal, i);
     // the warp's smallest limit decides whether a tile needs the comparison at all
-    const int lim_warp = masked_limit(m, p.s.causal, tile0 + (wq * 32) / pack);
+    const int lim_warp = masked_limit(m, p.s.causal, tile0 + ((wq * 32) >> p.s.pack_bits));
     const float sl2 = kTransform ? 1.0f : p.s.scale_log2;
     float slope = 0.0f;
     if constexpr (kBias) slope = __ldg(p.s.slopes + h) * 1.4426950408889634f;
@@ -593,11 +596,11 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       float m_of[2], l_of[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const int t0 = tok0 + (kAlt ? 0 : a * tile_tokens), query = t0 + row / pack;
+        const int t0 = tok0 + (kAlt ? 0 : a * tile_tokens), query = t0 + (row >> p.s.pack_bits);
         place_of[a] = query + m.nk - m.nq;
         lim_of[a] = masked_limit(m, p.s.causal, query);
-        lim_warp_of[a] = masked_limit(m, p.s.causal, t0 + (wq * 32) / pack);
-        live_of[a] = t0 + (wq * 32) / pack < m.nq;
+        lim_warp_of[a] = masked_limit(m, p.s.causal, t0 + ((wq * 32) >> p.s.pack_bits));
+        live_of[a] = t0 + ((wq * 32) >> p.s.pack_bits) < m.nq;
         m_of[a] = 0.0f;
         if constexpr (kBias) {  // of the keys [0, lim): the nearest, or with a negative slope the
                                 // farthest, has the largest bias
@@ -841,13 +844,13 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
           for (int r0 = 0; r0 < 32; r0 += 32 / kLanes) {
             const int r = wq * 32 + r0 + lane / kLanes;
             const int at = lane % kLanes;
-            const int tok = tile0 + r / pack;
+            const int tok = tile0 + (r >> p.s.pack_bits);
             if (tok < m.nq) {
               const uint4 v = *reinterpret_cast<const uint4*>(
                   stage + (at >> 3) * L::kBoxBytes + r * 128 + (((at & 7) ^ (r & 7)) << 4));
               *reinterpret_cast<uint4*>(p.out + b * p.out_stride[0] +
                                         (long long)(m.q0 + tok) * p.out_stride[1] +
-                                        (long long)(h0 + r % pack) * p.out_stride[2] + at * 8) = v;
+                                        (long long)(h0 + (r & (pack - 1))) * p.out_stride[2] + at * 8) = v;
             }
           }
           if (p.lse && valid)

@@ -156,6 +156,7 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
   s.kv_heads = a.kv_heads;
   s.group = a.heads / a.kv_heads;
   s.pack = s.group <= ltx::kBlockM && (s.group & (s.group - 1)) == 0 ? s.group : 1;
+  while ((1 << s.pack_bits) < s.pack) ++s.pack_bits;
   s.docs = a.docs;
   s.q_starts = a.q_starts;
   s.kv_starts = a.kv_starts;
@@ -626,6 +627,7 @@ int ltxattn_masked_backward(const ltxattn_masked_call* call, const ltxattn_maske
   ltx::MaskedBwdParams p{};
   p.s = shape_of(a, c);
   p.s.pack = 1;
+  p.s.pack_bits = 0;
   p.scale = a.scale;
   const BwdPlan f = plan_backward(p.s, d, a.softcap > 0.0f, c.num_sms);
   if (grid_ctas(f.units_kv, a.kv_heads, a.batch, f.parts_kv) > kMaxCtas ||
