@@ -501,10 +501,20 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         masked_scores<true, false>(s, p.s, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int x = 0; x < 64; ++x) bent[x] = cap_bend(s[x], inv_cap);
-        if constexpr (kBias)
-          masked_bias<true>(s, p.s, slope, (float)(i0 + (m.nk - m.nq) - j), 1.0f);
-      } else if constexpr (kBias) {
-        masked_bias<false>(s, p.s, slope, (float)(i0 + (m.nk - m.nq) - j), 1.0f);
+      }
+      if constexpr (kBias) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 32)
+          masked_bias<kCap, 32>(s + c, p.s, slope, (float)(i0 + c + (m.nk - m.nq) - j), 1.0f);
+      }
+      if (masked) {  // apart from the exponentials, which most tiles take without it
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          if (i0 + c0 >= from_warp) continue;
+#pragma unroll
+          for (int c = c0; c < c0 + 32; ++c)
+            if (i0 + c < from) s[c] = -INFINITY;
+        }
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -516,9 +526,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int q = c * 32 + x + y;
-            float a = kCap || kBias ? s[q] - l[y] : fmaf(s[q], p.s.scale_log2, -l[y]);
-            if (masked && i0 + q < from) a = -INFINITY;
-            w[x + y] = ex2(a);
+            w[x + y] = ex2(kCap || kBias ? s[q] - l[y] : fmaf(s[q], p.s.scale_log2, -l[y]));
             s[q] = kCap ? w[x + y] * bent[q] : w[x + y];
           }
         }
@@ -855,7 +863,8 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       if (i < m.nq) {
         const long long tok = m.q0 + i;
         const uint4* o = reinterpret_cast<const uint4*>(
-            p.out + b * p.out_stride[0] + tok * p.out_stride[1] + h * p.out_stride[2] + g * (D / 2));
+            p.out + b * p.out_stride[0] + tok * p.out_stride[1] + h * p.out_stride[2] +
+            g * (D / 2));
         const uint4* d = reinterpret_cast<const uint4*>(p.d_out + b * p.d_out_stride[0] +
                                                         tok * p.d_out_stride[1] +
                                                         h * p.d_out_stride[2] + g * (D / 2));
@@ -903,22 +912,31 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         masked_scores<true, false>(s, p.s, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int x = 0; x < 64; ++x) bent[x] = cap_bend(s[x], inv_cap);
-        if constexpr (kBias) masked_bias<true>(s, p.s, slope, (float)(place - kv0), -1.0f);
-      } else if constexpr (kBias) {
-        masked_bias<false>(s, p.s, slope, (float)(place - kv0), -1.0f);
+      }
+      if constexpr (kBias) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 32)
+          masked_bias<kCap, 32>(s + c, p.s, slope, (float)(place - kv0 - c), -1.0f);
+      }
+      if (masked) {  // apart from the exponentials, which most tiles take without it
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          if (kv0 + c0 + 32 <= lim_warp) continue;
+#pragma unroll
+          for (int c = c0; c < c0 + 32; ++c)
+            if (kv0 + c >= lim) s[c] = -INFINITY;
+        }
       }
 #pragma unroll
-      for (int c = 0; c < 64; ++c) {
-        float a = kCap || kBias ? s[c] - st.x : fmaf(s[c], p.s.scale_log2, -st.x);
-        if (masked && kv0 + c >= lim) a = -INFINITY;
-        s[c] = ex2(a);
-      }
+      for (int c = 0; c < 64; ++c)
+        s[c] = ex2(kCap || kBias ? s[c] - st.x : fmaf(s[c], p.s.scale_log2, -st.x));
       if constexpr (kFix) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float w[32];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) w[x] = kCap ? s[c * 32 + x] * bent[c * 32 + x] : s[c * 32 + x];
+          for (int x = 0; x < 32; ++x)
+            w[x] = kCap ? s[c * 32 + x] * bent[c * 32 + x] : s[c * 32 + x];
           store_operand<false>(trow + L::kColS + g * 64 + c * 32, w);
         }
         tmem_st_wait();

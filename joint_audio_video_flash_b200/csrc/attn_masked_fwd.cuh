@@ -227,12 +227,13 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   return r;
 }
 
-// Subtracts slope_log2 |far0 + dir c| from a thread's N scores, after the scale when they are
-// still raw (kScaled = false).  Whole warp.  Where no element of the warp lies on the
-// diagonal's other side, |distance| is linear in the column and takes one packed multiply-add.
+// Subtracts slope_log2 |far0 + dir c| from N of a thread's scores, after the scale when they are
+// still raw (kScaled = false).  Whole warp.  Where no element of the warp lies on the diagonal's
+// other side, |distance| is linear in the column and takes one packed multiply-add; a tile that
+// the warp's rows cross is taken 32 columns at a time.
 template <bool kScaled, int N>
-__device__ __forceinline__ void masked_bias(float (&s)[N], const MaskedShape& p,
-                                            float slope_log2, float far0, float dir) {
+__device__ __forceinline__ void masked_bias(float* s, const MaskedShape& p, float slope_log2,
+                                            float far0, float dir) {
   const float far1 = far0 + dir * (float)(N - 1);
   const bool ahead = __all_sync(0xffffffffu, fminf(far0, far1) >= 0.0f);
   const bool behind = __all_sync(0xffffffffu, fmaxf(far0, far1) <= 0.0f);
@@ -248,6 +249,10 @@ __device__ __forceinline__ void masked_bias(float (&s)[N], const MaskedShape& p,
       s[c] = r.x;
       s[c + 1] = r.y;
     }
+  } else if constexpr (N > 32) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32)
+      masked_bias<kScaled, 32>(s + c, p, slope_log2, far0 + dir * (float)c, dir);
   } else {
 #pragma unroll
     for (int c = 0; c < N; ++c)
@@ -321,7 +326,7 @@ __device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& 
       for (int c = 0; c < N; ++c) s[c] = tanh_ex2(s[c] * p.cap_in) * p.cap_log2;
     }
   }
-  if constexpr (kBias) masked_bias<kCap>(s, p, slope_log2, far0, dir);
+  if constexpr (kBias) masked_bias<kCap, N>(s, p, slope_log2, far0, dir);
 }
 
 // The largest cap (log2 units) whose scores need no running maximum: weights 2^s between 2^-90
@@ -702,8 +707,12 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
         if (kv0 + kBlockN > lim_warp) {
           const int to = lim - kv0;
 #pragma unroll
-          for (int c = 0; c < kBlockN; ++c)
-            if (c >= to) s[c] = -INFINITY;
+          for (int c0 = 0; c0 < kBlockN; c0 += 32) {
+            if (kv0 + c0 + 32 <= lim_warp) continue;
+#pragma unroll
+            for (int c = c0; c < c0 + 32; ++c)
+              if (c >= to) s[c] = -INFINITY;
+          }
         }
         float mx = row_max<kBlockN>(s) * sl2;
         if (step == 0) {
@@ -850,7 +859,8 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
                   stage + (at >> 3) * L::kBoxBytes + r * 128 + (((at & 7) ^ (r & 7)) << 4));
               *reinterpret_cast<uint4*>(p.out + b * p.out_stride[0] +
                                         (long long)(m.q0 + tok) * p.out_stride[1] +
-                                        (long long)(h0 + (r & (pack - 1))) * p.out_stride[2] + at * 8) = v;
+                                        (long long)(h0 + (r & (pack - 1))) * p.out_stride[2] +
+                                        at * 8) = v;
             }
           }
           if (p.lse && valid)

@@ -327,7 +327,9 @@ struct BwdPlan {
 
 // Whether the dQ kernel carries the sum that takes out's rounding off dQ (attn_masked_bwd.cuh):
 // where scores are capped or biased, or rows have few keys, or P and dS are exact.
-bool dq_fix(const ltx::MaskedShape& s, bool cap) { return cap || s.slopes || fine(s) || few_keys(s); }
+bool dq_fix(const ltx::MaskedShape& s, bool cap) {
+  return cap || s.slopes || fine(s) || few_keys(s);
+}
 
 BwdPlan plan_backward(const ltx::MaskedShape& s, int head_dim, bool cap, int num_sms) {
   BwdPlan f;
