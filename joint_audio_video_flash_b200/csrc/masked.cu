@@ -147,6 +147,18 @@ size_t lse_bytes(const ltxattn_masked_call& a) {
   return (size_t)a.batch * a.heads * a.q_len * 4;
 }
 
+// Rows of a token in a tile: the group of query heads rounded up to a power of two where that
+// makes no more tiles of `queries` queries than a head at a time (a group of 2^n never does).
+int pack_of(int queries, int group) {
+  int pack = 1;
+  while (pack < group) pack *= 2;
+  if (pack > ltx::kBlockM) return 1;
+  if (pack == group) return pack;
+  const long long n = std::max(queries, 1);
+  const long long packed = (n * pack + ltx::kBlockM - 1) / ltx::kBlockM;
+  return packed < group * ((n + ltx::kBlockM - 1) / ltx::kBlockM) ? pack : 1;
+}
+
 ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext& c) {
   ltx::MaskedShape s{};
   s.batch = a.batch;
@@ -155,8 +167,9 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
   s.heads = a.heads;
   s.kv_heads = a.kv_heads;
   s.group = a.heads / a.kv_heads;
-  s.pack = s.group <= ltx::kBlockM && (s.group & (s.group - 1)) == 0 ? s.group : 1;
+  s.pack = pack_of(a.q_len / std::max(a.docs, 1), s.group);
   while ((1 << s.pack_bits) < s.pack) ++s.pack_bits;
+  s.tile_heads = s.pack > 1 ? s.kv_heads : s.heads;
   s.docs = a.docs;
   s.q_starts = a.q_starts;
   s.kv_starts = a.kv_starts;
@@ -249,7 +262,7 @@ FwdPlan plan_forward(const ltx::MaskedShape& s, int head_dim, int num_sms) {
   const long long docs = std::max(s.docs, 1);
   const long long tiles = std::max<long long>(
       1, (s.kv_len / docs + ltx::kBlockN - 1) / ltx::kBlockN);
-  const long long per_head = (long long)(s.heads / s.pack) * s.batch;
+  const long long per_head = (long long)s.tile_heads * s.batch;
   // partials written and read at 6 TB/s
   const long long part_bytes = (long long)s.batch * s.heads * s.q_len * (head_dim + 1) * 8;
   FwdPlan best{};
@@ -282,7 +295,7 @@ size_t partial_bytes(const ltx::MaskedShape& s, int head_dim, int parts) {
 template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>
 cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const ltx::MaskedFwdParams& p, int units, cudaStream_t stream) {
-  const unsigned grid = (unsigned)grid_ctas(units, p.s.heads / p.s.pack, p.s.batch, p.parts);
+  const unsigned grid = (unsigned)grid_ctas(units, p.s.tile_heads, p.s.batch, p.parts);
   ltx::ltx_masked_fwd<D, kAlt, kCap, kBias, kFixed>
       <<<grid, ltx::kMaskedThreads, ltx::MaskedSmem<D, kAlt>::kAlloc, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
@@ -564,7 +577,7 @@ int ltxattn_masked_forward(const ltxattn_masked_call* call, void* workspace,
   p.lse = a.lse;
   const FwdPlan f = plan_forward(p.s, a.head_dim, c.num_sms);
   p.parts = f.parts;
-  if (grid_ctas(f.units, a.heads / p.s.pack, a.batch, f.parts) > kMaxCtas)
+  if (grid_ctas(f.units, p.s.tile_heads, a.batch, f.parts) > kMaxCtas)
     return LTXATTN_ERR_UNSUPPORTED;
   const size_t need = partial_bytes(p.s, a.head_dim, f.parts);
   if (need > 0) {
@@ -630,6 +643,7 @@ int ltxattn_masked_backward(const ltxattn_masked_call* call, const ltxattn_maske
   p.s = shape_of(a, c);
   p.s.pack = 1;
   p.s.pack_bits = 0;
+  p.s.tile_heads = p.s.heads;
   p.scale = a.scale;
   const BwdPlan f = plan_backward(p.s, d, a.softcap > 0.0f, c.num_sms);
   if (grid_ctas(f.units_kv, a.kv_heads, a.batch, f.parts_kv) > kMaxCtas ||

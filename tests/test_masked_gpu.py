@@ -315,6 +315,29 @@ def test_caps_far_from_the_scores(kv_len):
     assert all(torch.isfinite(t).all() for t in run_backward(q, k, v, d_out, opts).values())
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [3, 5, 7, 24, 96, 130])
+def test_groups_of_every_size(group, dim):
+    """Groups of query heads that fill a power of two of rows or do not, with heads of another
+    group (or none) behind them."""
+    for q_len, kv_len, kv_heads, o in ((1, 700, 2, dict(causal=True, bias=True)), (9, 300, 1, {}),
+                                       (70, 90, 2, dict(causal=True, cap=5.0))):
+        if group > 24 and q_len > 9:
+            continue
+        q, k, v, _ = make(2, q_len, kv_len, kv_heads * group, kv_heads, dim)
+        opts = options(kv_heads * group, **o)
+        compare(run(q, k, v, opts), block_ops.masked(q, k, v, **opts), ("out", "lse"))
+    # packed documents, some without a query; rows of no document keep their marks
+    q, k, v, _ = make(1, 60, 400, 2 * group, 2, dim)
+    opts = options(2 * group, q_starts=starts([[-3, 1, 0, 30, 9, 10]]),
+                   kv_starts=starts([[-8, 100, 50, 1, 200, 20]]))
+    ref = block_ops.masked(q, k, v, **opts)
+    got = run(q, k, v, opts)
+    compare(got, ref, ("out", "lse"))
+    assert torch.all(got["out"].cpu()[torch.isnan(ref["out"])] == 7)
+    assert torch.all(got["lse"].cpu()[torch.isnan(ref["lse"])] == 5)
+
+
 LONG = [
     # rows of more keys than the form without a running maximum starts at, in both plans
     (1, 150, 4200, 2, 2, 64, dict(causal=True, cap=30.0)),
