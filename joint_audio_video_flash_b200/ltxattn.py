@@ -144,7 +144,7 @@ def _check(status: int, where: str) -> None:
 
 
 def create() -> None:
-    _check(load().ltxattn_create(), "ltxattn_create")
+    _check((_lib or load()).ltxattn_create(), "ltxattn_create")
 
 
 def destroy() -> None:
@@ -461,8 +461,18 @@ def combine(o_parts, lses, q_len: int, out=None, *, stream=None):
 BF16, FP16, FP32 = 0, 1, 2
 ROPE_LAYOUTS = {"pairs": 0, "halves": 1}
 
+_NO_STRIDES = (0, 0, 0)
+
 # The calls below run at the size of one token too, where the host's time is the call's time:
-# a tensor is looked at once, and the current device and stream are asked for once a call.
+# a tensor is looked at once, one that is made here not at all, and the current device and stream
+# are asked for once a call.
+
+
+def _raw_stream(device: int) -> int:
+    """The current stream's handle."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
 
 @functools.lru_cache(maxsize=1)
 def _dtype_codes() -> dict:
@@ -477,38 +487,18 @@ def _dtype_code(t) -> int:
     return code
 
 
-class _OnStream:
-    """The current device (``device``) and the stream a call runs on (``handle``).  Allocations
-    inside the with-block belong to that stream (torch's allocator reuses their memory in that
-    stream's order), and tensors given to ``used`` are not handed out again before the work
-    queued on it is done."""
-    __slots__ = ("device", "handle", "stream", "scope")
-
-    def __init__(self, stream):
-        import torch
-        self.device = torch.cuda.current_device()
-        self.handle = torch._C._cuda_getCurrentRawStream(self.device)
-        self.stream = self.scope = None
-        if stream is not None and int(stream.cuda_stream) != self.handle:
-            self.handle = int(stream.cuda_stream)
-            self.stream = stream
-            self.scope = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.scope is not None:
-            self.scope.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.scope is not None:
-            self.scope.__exit__(*exc)
-        return False
-
-    def used(self, *tensors) -> None:
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+def _on_stream(stream, call, *args, **kw):
+    """``call`` on another stream than the current one: allocations inside belong to that stream
+    (torch's allocator reuses their memory in that stream's order), and the tensors it was given
+    are not handed out again before the work queued on it is done."""
+    import torch
+    with torch.cuda.stream(stream):
+        result = call(*args, **kw)
+    if stream != torch.cuda.current_stream():
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return result
 
 
 def _not_here(name: str, t, dtype, device: int):
@@ -549,7 +539,7 @@ def _heads_strides(name: str, t, device: int, dtype, shape=None):
     strides = t.stride()
     if strides[3] != 1 and size[3] > 1:
         raise ValueError(f"the channels of {name} must be contiguous")
-    return strides[:3]
+    return strides
 
 
 def rope_frequencies(axis_dims, base: float = 10000.0) -> list[float]:
@@ -582,44 +572,54 @@ def rope_axes(q, k, positions, inv_freq, axis_dims, q_out=None, k_out=None, *,
     the gradient.  The outputs may be the inputs (in place).
     """
     import torch
+    if stream is not None:
+        return _on_stream(stream, rope_axes, q, k, positions, inv_freq, axis_dims, q_out, k_out,
+                          layout=layout, inverse=inverse)
     freq, freq_at, dims = _rope_axes_arrays(tuple(inv_freq), tuple(axis_dims))
     axes = len(axis_dims)
     code_layout = ROPE_LAYOUTS.get(layout)
     if code_layout is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    with _OnStream(stream) as on:
-        device = on.device
-        q_strides = _heads_strides("q", q, device, None)
-        code = _dtype_code(q)
-        shape = q.shape
-        batch, length, heads, head_dim = shape
-        _check_cuda("positions", positions, device, torch.float32)
-        pos_batch = positions.shape[0] if positions.dim() == 3 else 0
-        if pos_batch not in (1, batch) or positions.shape[1:] != (length, axes):
-            raise ValueError(f"positions must be [{batch} or 1, {length}, {axes}]")
-        if q_out is None:
-            q_out = torch.empty_like(q)
+    device = torch.cuda.current_device()
+    q_strides = _heads_strides("q", q, device, None)
+    code = _dtype_code(q)
+    shape = q.shape
+    batch, length, heads, head_dim = shape
+    _check_cuda("positions", positions, device, torch.float32)
+    pos_shape = positions.shape
+    pos_batch = pos_shape[0]
+    if len(pos_shape) != 3 or pos_batch not in (1, batch) or pos_shape[1] != length \
+            or pos_shape[2] != axes:
+        raise ValueError(f"positions must be [{batch} or 1, {length}, {axes}]")
+    if q_out is None:
+        q_out = torch.empty_like(q)
+        q_out_strides = q_out.stride()
+    else:
         q_out_strides = _heads_strides("q_out", q_out, device, q.dtype, shape)
-        kv_heads, k_strides, k_out_strides = 1, (0, 0, 0), (0, 0, 0)
-        if k is not None:
-            k_strides = _heads_strides("k", k, device, None)
-            k_shape = k.shape
-            if k.dtype != q.dtype or k_shape[0] != batch or k_shape[1] != length \
-                    or k_shape[3] != head_dim:
-                raise ValueError("k must have q's dtype, batch, length and head_dim")
-            kv_heads = k_shape[2]
-            if k_out is None:
-                k_out = torch.empty_like(k)
-            k_out_strides = _heads_strides("k_out", k_out, device, k.dtype, k_shape)
-        elif k_out is not None:
-            raise ValueError("k_out without k")
-        call = _pack_rope(
-            q.data_ptr(), 0 if k is None else k.data_ptr(), q_out.data_ptr(),
-            0 if k is None else k_out.data_ptr(), *q_strides, *k_strides, *q_out_strides,
-            *k_out_strides, positions.data_ptr(), freq_at, *dims, axes, pos_batch, batch, length,
-            heads, kv_heads, head_dim, code, code_layout, bool(inverse))
-        _check(load().ltxattn_rope_axes(call, on.handle), "ltxattn_rope_axes")
-        on.used(q, k, q_out, k_out, positions)
+    if k is not None:
+        k_strides = _heads_strides("k", k, device, None)
+        k_shape = k.shape
+        kv_heads = k_shape[2]
+        if k.dtype != q.dtype or k_shape[0] != batch or k_shape[1] != length \
+                or k_shape[3] != head_dim:
+            raise ValueError("k must have q's dtype, batch, length and head_dim")
+        if k_out is None:
+            k_out = torch.empty_like(k)
+            k_out_strides = k_out.stride()
+        else:
+            k_out_strides = _heads_strides("k_out", k_out, device, q.dtype, k_shape)
+        k_at, k_out_at = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    else:
+        kv_heads, k_strides, k_out_strides, k_at, k_out_at = 1, _NO_STRIDES, _NO_STRIDES, 0, 0
+    call = _pack_rope(
+        q.data_ptr(), k_at, q_out.data_ptr(), k_out_at, *q_strides[:3], *k_strides[:3],
+        *q_out_strides[:3], *k_out_strides[:3], positions.data_ptr(), freq_at, *dims, axes,
+        pos_batch, batch, length, heads, kv_heads, head_dim, code, code_layout, bool(inverse))
+    status = (_lib or load()).ltxattn_rope_axes(call, _raw_stream(device))
+    if status:
+        _check(status, "ltxattn_rope_axes")
     return q_out, k_out
 
 
@@ -683,22 +683,26 @@ def layer_norm(x, weight=None, bias=None, out=None, *, eps: float = 1e-6,
     ``out`` may be x.
     """
     import torch
-    with _OnStream(stream) as on:
-        rows, cols, x_stride = _norm_rows("x", x, on.device)
-        code = _dtype_code(x)
-        groups = _norm_affine(weight, bias, x, rows, cols, on.device)
-        if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-            out_stride = cols
-        else:
-            out_stride = _norm_rows("out", out, on.device, x.dtype, x.shape)[2]
-        mean = rstd = None
-        if return_stats:
-            mean, rstd = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
-        _check(load().ltxattn_layer_norm(
-            x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean), _ptr(rstd), rows,
-            cols, groups, x_stride, out_stride, eps, code, on.handle), "ltxattn_layer_norm")
-        on.used(x, weight, bias, out)
+    if stream is not None:
+        return _on_stream(stream, layer_norm, x, weight, bias, out, eps=eps,
+                          return_stats=return_stats)
+    device = torch.cuda.current_device()
+    rows, cols, x_stride = _norm_rows("x", x, device)
+    code = _dtype_code(x)
+    groups = _norm_affine(weight, bias, x, rows, cols, device)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out_stride = cols
+    else:
+        out_stride = _norm_rows("out", out, device, x.dtype, x.shape)[2]
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = torch.empty(2, *x.shape[:-1], dtype=torch.float32, device=x.device)
+    status = (_lib or load()).ltxattn_layer_norm(
+        x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean), _ptr(rstd), rows,
+        cols, groups, x_stride, out_stride, eps, code, _raw_stream(device))
+    if status:
+        _check(status, "ltxattn_layer_norm")
     return (out, mean, rstd) if return_stats else out
 
 
@@ -710,37 +714,37 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, *, stream=None)
     or x.
     """
     import torch
-    lib = load()
-    with _OnStream(stream) as on:
-        device = on.device
-        rows, cols, x_stride = _norm_rows("x", x, device)
-        code = _dtype_code(x)
-        dy_stride = _norm_rows("dy", dy, device, x.dtype, x.shape)[2]
-        stats = x.shape[:-1]
-        _check_cuda("mean", mean, device, torch.float32, stats)
-        _check_cuda("rstd", rstd, device, torch.float32, stats)
-        groups = _norm_affine(weight, None, x, rows, cols, device)
-        if dx is None:
-            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-            dx_stride = cols
-        else:
-            dx_stride = _norm_rows("dx", dx, device, x.dtype, x.shape)[2]
-        dweight = dbias = workspace = None
-        need = ctypes.c_ulonglong(0)
-        if weight is not None:
-            dweight = torch.empty_like(weight, dtype=torch.float32)
-            dbias = torch.empty_like(dweight)
-            _check(lib.ltxattn_layer_norm_workspace(rows, cols, groups, code,
-                                                    ctypes.byref(need)),
-                   "ltxattn_layer_norm_workspace")
-            if need.value:
-                workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        _check(lib.ltxattn_layer_norm_backward(
-            dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
-            dx.data_ptr(), _ptr(dweight), _ptr(dbias), rows, cols, groups, dy_stride, x_stride,
-            dx_stride, code, _ptr(workspace), need.value, on.handle),
-            "ltxattn_layer_norm_backward")
-        on.used(dy, x, mean, rstd, weight, dx)
+    if stream is not None:
+        return _on_stream(stream, layer_norm_backward, dy, x, mean, rstd, weight, dx)
+    lib = _lib or load()
+    device = torch.cuda.current_device()
+    rows, cols, x_stride = _norm_rows("x", x, device)
+    code = _dtype_code(x)
+    dy_stride = _norm_rows("dy", dy, device, x.dtype, x.shape)[2]
+    stats = x.shape[:-1]
+    _check_cuda("mean", mean, device, torch.float32, stats)
+    _check_cuda("rstd", rstd, device, torch.float32, stats)
+    groups = _norm_affine(weight, None, x, rows, cols, device)
+    if dx is None:
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        dx_stride = cols
+    else:
+        dx_stride = _norm_rows("dx", dx, device, x.dtype, x.shape)[2]
+    dweight = dbias = workspace = None
+    need = ctypes.c_ulonglong(0)
+    if weight is not None:
+        dweight = torch.empty_like(weight, dtype=torch.float32)
+        dbias = torch.empty_like(dweight)
+        _check(lib.ltxattn_layer_norm_workspace(rows, cols, groups, code, need),
+               "ltxattn_layer_norm_workspace")
+        if need.value:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+    status = lib.ltxattn_layer_norm_backward(
+        dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
+        dx.data_ptr(), _ptr(dweight), _ptr(dbias), rows, cols, groups, dy_stride, x_stride,
+        dx_stride, code, _ptr(workspace), need.value, _raw_stream(device))
+    if status:
+        _check(status, "ltxattn_layer_norm_backward")
     return dx, dweight, dbias
 
 
@@ -757,7 +761,8 @@ def _masked_call(device, q, k, v, out, lse, scale, softcap, slopes, causal, pref
     k_strides = _heads_strides("k", k, device, bf16)
     q_shape, k_shape = q.shape, k.shape
     batch, q_len, heads, head_dim = q_shape
-    if k_shape[0] != batch or k_shape[3] != head_dim or v.shape != k_shape:
+    kv_batch, kv_len, kv_heads, kv_dim = k_shape
+    if kv_batch != batch or kv_dim != head_dim or v.shape != k_shape:
         raise ValueError("k and v must be [batch, kv_len, kv_heads, head_dim] matching q")
     v_strides = _heads_strides("v", v, device, bf16)
     out_strides = _heads_strides("out", out, device, bf16, q_shape)
@@ -778,8 +783,8 @@ def _masked_call(device, q, k, v, out, lse, scale, softcap, slopes, causal, pref
     if slopes is not None:
         _check_cuda("slopes", slopes, device, torch.float32, (heads,))
     return _pack_masked(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *q_strides,
-        *k_strides, *v_strides, *out_strides, batch, q_len, k_shape[1], heads, k_shape[2],
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *q_strides[:3],
+        *k_strides[:3], *v_strides[:3], *out_strides[:3], batch, q_len, kv_len, heads, kv_heads,
         head_dim, 1.0 / math.sqrt(head_dim) if scale is None else scale, softcap,
         0 if slopes is None else slopes.data_ptr(), 0 if prefix is None else prefix.data_ptr(),
         0 if docs == 0 else q_starts.data_ptr(), 0 if docs == 0 else kv_starts.data_ptr(), docs,
@@ -810,24 +815,28 @@ def masked_forward(q, k, v, out=None, lse=None, *, scale: float | None = None,
     when they are allocated here).
     """
     import torch
-    with _OnStream(stream) as on:
-        if out is None or lse is None:  # rows of no document stay as they are made here
-            _heads_strides("q", q, on.device, torch.bfloat16)
-            if out is None:
-                out = torch.empty_like(q) if q_starts is None else torch.zeros_like(q)
-            if lse is None:
-                shape = (q.shape[0], q.shape[2], q.shape[1])
-                lse = torch.empty(shape, dtype=torch.float32, device=q.device) \
-                    if q_starts is None else \
-                    torch.full(shape, -math.inf, dtype=torch.float32, device=q.device)
-        call = _masked_call(on.device, q, k, v, out, lse, scale, softcap, slopes, causal, prefix,
-                            q_starts, kv_starts)
-        lib = load()
-        workspace, need = _masked_workspace(lib, call, False, q.device)
-        _check(lib.ltxattn_masked_forward(
-            call, None if workspace is None else workspace.data_ptr(), need, on.handle),
-            "ltxattn_masked_forward")
-        on.used(q, k, v, out, lse, slopes, prefix, q_starts, kv_starts)
+    if stream is not None:
+        return _on_stream(stream, masked_forward, q, k, v, out, lse, scale=scale, softcap=softcap,
+                          slopes=slopes, causal=causal, prefix=prefix, q_starts=q_starts,
+                          kv_starts=kv_starts)
+    device = torch.cuda.current_device()
+    if out is None or lse is None:  # rows of no document stay as they are made here
+        _heads_strides("q", q, device, torch.bfloat16)
+        if out is None:
+            out = torch.empty_like(q) if q_starts is None else torch.zeros_like(q)
+        if lse is None:
+            shape = (q.shape[0], q.shape[2], q.shape[1])
+            lse = torch.empty(shape, dtype=torch.float32, device=q.device) \
+                if q_starts is None else \
+                torch.full(shape, -math.inf, dtype=torch.float32, device=q.device)
+    call = _masked_call(device, q, k, v, out, lse, scale, softcap, slopes, causal, prefix,
+                        q_starts, kv_starts)
+    lib = _lib or load()
+    workspace, need = _masked_workspace(lib, call, False, q.device)
+    status = lib.ltxattn_masked_forward(call, None if workspace is None else workspace.data_ptr(),
+                                        need, _raw_stream(device))
+    if status:
+        _check(status, "ltxattn_masked_forward")
     return out, lse
 
 
@@ -843,24 +852,30 @@ def masked_backward(d_out, q, k, v, out, lse, dq=None, dk=None, dv=None, *,
     import torch
     if out is None or lse is None:
         raise ValueError("out and lse of the forward call are needed")
-    with _OnStream(stream) as on:
-        device, bf16 = on.device, torch.bfloat16
-        call = _masked_call(device, q, k, v, out, lse, scale, softcap, slopes, causal, prefix,
-                            q_starts, kv_starts)
-        d_out_strides = _heads_strides("d_out", d_out, device, bf16, q.shape)
-        make = torch.empty_like if q_starts is None else torch.zeros_like
-        grads, strides = [], []
-        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-            if t is None:
-                t = make(like)
+    if stream is not None:
+        return _on_stream(stream, masked_backward, d_out, q, k, v, out, lse, dq, dk, dv,
+                          scale=scale, softcap=softcap, slopes=slopes, causal=causal,
+                          prefix=prefix, q_starts=q_starts, kv_starts=kv_starts)
+    device, bf16 = torch.cuda.current_device(), torch.bfloat16
+    call = _masked_call(device, q, k, v, out, lse, scale, softcap, slopes, causal, prefix,
+                        q_starts, kv_starts)
+    d_out_strides = _heads_strides("d_out", d_out, device, bf16, q.shape)
+    make = torch.empty_like if q_starts is None else torch.zeros_like
+    grads, strides = [], []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is None:
+            t = make(like)
+            strides.append(t.stride())
+        else:
             strides.append(_heads_strides(name, t, device, bf16, like.shape))
-            grads.append(t)
-        dq, dk, dv = grads
-        grad = _pack_grad(d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                          *d_out_strides, *strides[0], *strides[1], *strides[2])
-        lib = load()
-        workspace, need = _masked_workspace(lib, call, True, q.device)
-        _check(lib.ltxattn_masked_backward(call, grad, workspace.data_ptr(), need, on.handle),
-               "ltxattn_masked_backward")
-        on.used(d_out, q, k, v, out, lse, dq, dk, dv, slopes, prefix, q_starts, kv_starts)
+        grads.append(t)
+    dq, dk, dv = grads
+    grad = _pack_grad(d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                      *d_out_strides[:3], *strides[0][:3], *strides[1][:3], *strides[2][:3])
+    lib = _lib or load()
+    workspace, need = _masked_workspace(lib, call, True, q.device)
+    status = lib.ltxattn_masked_backward(call, grad, workspace.data_ptr(), need,
+                                         _raw_stream(device))
+    if status:
+        _check(status, "ltxattn_masked_backward")
     return dq, dk, dv
