@@ -210,6 +210,27 @@ struct BwdKvSmem {
   static constexpr uint32_t kTmemCols = 512;
 };
 
+// The query tiles that see a key of a tile: from tile qt0 on.  The walk goes over them head after
+// head, and this CTA takes steps [begin, begin + n) of it.
+struct MaskedKvWalk {
+  int j0, n_qt, qt0, per_head, begin, n;
+};
+
+__device__ __forceinline__ MaskedKvWalk masked_kv_walk(const MaskedDoc& m,
+                                                       const MaskedBwdParams& p, int part) {
+  MaskedKvWalk w;
+  w.j0 = m.tile * kBlockN;
+  w.n_qt = (m.nq + kBlockM - 1) / kBlockM;
+  w.qt0 = 0;
+  if (p.s.causal && w.j0 >= m.prefix) w.qt0 = max(w.j0 - (m.nk - m.nq), 0) / kBlockM;
+  w.per_head = max(w.n_qt - w.qt0, 0);
+  const int total = w.per_head * p.s.group;  // group <= 1024, tiles <= 2^17: below 2^27
+  const int per_part = (total + p.parts - 1) / p.parts;
+  w.begin = min(part * per_part, total);
+  w.n = min(w.begin + per_part, total) - w.begin;
+  return w;
+}
+
 template <int D, bool kCap, bool kBias, bool kFine>
 __global__ void __launch_bounds__(kMaskedThreads, 1)
     ltx_masked_bwd_kv(const __grid_constant__ CUtensorMap tm_q,
@@ -232,38 +253,59 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
   const MaskedPlace at_work = masked_place(p.s.kv_heads, p.s.batch, p.parts);
   const int hk = at_work.head, b = at_work.b, part = at_work.part;
 
-  grid_dependency_wait();
-  // one barrier ahead of the work: what each warp prepares does not need the others
+  auto load_box = [&](uint32_t at, const CUtensorMap* map, int ready, int head, int row) {
+    mbar_arrive_expect_tx(bar(ready), L::kTileBytes);
+    for (int bx = 0; bx < L::kBoxes; ++bx)
+      tma_load_4d(sbase + at + bx * L::kBoxBytes, map, bar(ready), bx * 64, head, row, b);
+  };
+  // one barrier ahead of the work: what each warp prepares does not need the others, and the
+  // first tiles are on their way before it.  The kernel before this one in the stream wrote
+  // none of what they hold; only the softmax warps read what it wrote.
+  bool started = false;  // thread 0: they are
   if (warp == 1) {
     tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
     tmem_relinquish();
-  } else if (warp == 2) {
+  } else if (warp == 0) {
+    int status = kDevOk;
+    if (lane == 0) {
+      status = *reinterpret_cast<volatile int*>(p.s.status);
+      mbar_init(bar(L::bKF), 1);
+      mbar_init(bar(L::bVF), 1);
+      for (int s = 0; s < L::kStages; ++s) {
+        mbar_init(bar(L::bQF + s), 1);
+        mbar_init(bar(L::bQE + s), 1);
+        mbar_init(bar(L::bOF + s), 1);
+        mbar_init(bar(L::bOE + s), 1);
+      }
+      mbar_init(bar(L::bS), 1);
+      mbar_init(bar(L::bDp), 1);
+      for (int g = 0; g < 2; ++g) {
+        mbar_init(bar(L::bP + g), 4);
+        mbar_init(bar(L::bDs + g), 4);
+      }
+      mbar_init(bar(L::bEnd), 1);
+      mbar_init(bar(L::bDrain), 1);
+      fence_mbar_init();
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
     const MaskedDoc m = masked_find<true>(p.s, b, at_work.unit, kBlockN);
-    if (lane == 0) *shared_doc = m;
-  } else if (threadIdx.x == 0) {
-    const int status = *reinterpret_cast<volatile int*>(p.s.status);
-    mbar_init(bar(L::bKF), 1);
-    mbar_init(bar(L::bVF), 1);
-    for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(bar(L::bQF + s), 1);
-      mbar_init(bar(L::bQE + s), 1);
-      mbar_init(bar(L::bOF + s), 1);
-      mbar_init(bar(L::bOE + s), 1);
+    if (lane == 0) {
+      *shared_doc = m;
+      *abort_flag = status != kDevOk ? 1 : 0;
+      if (status == kDevOk && m.tile >= 0) {
+        const MaskedKvWalk w = masked_kv_walk(m, p, part);
+        if (w.n > 0) {
+          const int h = hk * p.s.group + w.begin / w.per_head;
+          const int row = m.q0 + (w.qt0 + w.begin % w.per_head) * kBlockM;
+          load_box(L::kK, &tm_k, L::bKF, hk, m.k0 + w.j0);
+          load_box(L::kQ, &tm_q, L::bQF, h, row);
+          load_box(L::kV, &tm_v, L::bVF, hk, m.k0 + w.j0);
+          load_box(L::kDo, &tm_do, L::bOF, h, row);
+          started = true;
+        }
+      }
     }
-    mbar_init(bar(L::bS), 1);
-    mbar_init(bar(L::bDp), 1);
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(bar(L::bP + g), 4);
-      mbar_init(bar(L::bDs + g), 4);
-    }
-    mbar_init(bar(L::bEnd), 1);
-    mbar_init(bar(L::bDrain), 1);
-    fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-    tma_prefetch_desc(&tm_do);
-    *abort_flag = status != kDevOk ? 1 : 0;
   }
   grid_dependents_launch();
   tc_fence_before();
@@ -277,56 +319,35 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
   }
   const WaitCtl ctl{abort_flag, p.s.status, p.s.timeout_ns};
 
-  // the query tiles that see a key of this tile: from tile `qt0` on; the walk goes over them
-  // head after head, and this CTA takes steps [begin, begin + n) of it
-  const int j0 = m.tile * kBlockN;
-  const int n_qt = (m.nq + kBlockM - 1) / kBlockM;
-  int qt0 = 0;
-  if (p.s.causal && j0 >= m.prefix) qt0 = max(j0 - (m.nk - m.nq), 0) / kBlockM;
-  const int per_head = max(n_qt - qt0, 0);
-  const int total = per_head * p.s.group;  // group <= 1024, tiles <= 2^17: below 2^27
-  const int per_part = (total + p.parts - 1) / p.parts;
-  const int begin = min(part * per_part, total);
-  const int n = min(begin + per_part, total) - begin;
+  const MaskedKvWalk walk = masked_kv_walk(m, p, part);
+  const int j0 = walk.j0, n_qt = walk.n_qt, qt0 = walk.qt0, per_head = walk.per_head;
+  const int begin = walk.begin, n = walk.n;
 
   if (warp < 4) {
     setmaxnreg_dec<kMaskedRegsProducer>();
-    if (warp == 0 && lane == 0 && n > 0 && !*abort_flag) {
+    if (started) {
       // ---------------------------------------------------------- TMA producer
-      mbar_arrive_expect_tx(bar(L::bKF), L::kTileBytes);
-      for (int bx = 0; bx < L::kBoxes; ++bx)
-        tma_load_4d(sbase + L::kK + bx * L::kBoxBytes, &tm_k, bar(L::bKF), bx * 64, hk,
-                    m.k0 + j0, b);
-      mbar_arrive_expect_tx(bar(L::bVF), L::kTileBytes);
-      for (int bx = 0; bx < L::kBoxes; ++bx)
-        tma_load_4d(sbase + L::kV + bx * L::kBoxBytes, &tm_v, bar(L::bVF), bx * 64, hk,
-                    m.k0 + j0, b);
       int last[L::kStages], last_o[L::kStages];
       for (int s = 0; s < L::kStages; ++s) last[s] = last_o[s] = -1;
+      last[0] = last_o[0] = 0;
       int h = hk * p.s.group + begin / per_head, qt = qt0 + begin % per_head;
       bool ok = true;
-      for (int t = 0; t < n && ok; ++t) {
+      for (int t = 1; t < n && ok; ++t) {
+        if (++qt == n_qt) {
+          qt = qt0;
+          ++h;
+        }
         const int st = t % L::kStages;
         const uint32_t ph = (uint32_t)(t / L::kStages) & 1u;
         const int row = m.q0 + qt * kBlockM;
         ok = mbar_wait_lean(bar(L::bQE + st), ph ^ 1u, ctl);
         if (!ok) break;
-        mbar_arrive_expect_tx(bar(L::bQF + st), L::kTileBytes);
-        for (int bx = 0; bx < L::kBoxes; ++bx)
-          tma_load_4d(sbase + L::kQ + st * L::kTileBytes + bx * L::kBoxBytes, &tm_q,
-                      bar(L::bQF + st), bx * 64, h, row, b);
+        load_box(L::kQ + st * L::kTileBytes, &tm_q, L::bQF + st, h, row);
         last[st] = t;
         ok = mbar_wait_lean(bar(L::bOE + st), ph ^ 1u, ctl);
         if (!ok) break;
-        mbar_arrive_expect_tx(bar(L::bOF + st), L::kTileBytes);
-        for (int bx = 0; bx < L::kBoxes; ++bx)
-          tma_load_4d(sbase + L::kDo + st * L::kTileBytes + bx * L::kBoxBytes, &tm_do,
-                      bar(L::bOF + st), bx * 64, h, row, b);
+        load_box(L::kDo + st * L::kTileBytes, &tm_do, L::bOF + st, h, row);
         last_o[st] = t;
-        if (++qt == n_qt) {
-          qt = qt0;
-          ++h;
-        }
       }
       if (!ok) {
         for (int s = 0; s < L::kStages; ++s) {
@@ -471,6 +492,7 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
       }
     };
     bool ok = !*abort_flag;
+    grid_dependency_wait();
     if (n > 0) fetch(h, qt);
     for (int t = 0; t < n && ok; ++t) {
       float* mine = stat + (t & 1) * 128;
