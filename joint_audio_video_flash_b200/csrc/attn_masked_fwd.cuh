@@ -314,7 +314,7 @@ __device__ __forceinline__ void cap_all(float (&s)[N], const MaskedShape& p) {
 // fits of tanh on these ranges, reweighted until the ripples are level).  The argument is scaled
 // first: folded into the coefficients the scale takes them below fp32's range from a cap of 60
 // on.  Measured at 8192 x 8192 x 16 heads x 128, N(0, 1) scores, with a running maximum: 1229 us
-// with tanh_ex2 alone, 800 us with degree 11 alone, 720 us.
+// with tanh_ex2 alone, 800 us with degree 11 alone, 740 us.
 template <bool kCap, bool kBias, int N>
 __device__ __forceinline__ void masked_scores(float (&s)[N], const MaskedShape& p,
                                               float slope_log2, float far0, float dir) {
@@ -342,8 +342,8 @@ constexpr float kFixedMaxCap = 90.0f;
 // of O, and nothing that two threads would have to agree on before they use it.  So the two
 // softmax warpgroups share every tile, 64 keys each, instead of a tile each: a tile's softmax,
 // long because of the cap, takes half the time, and the tensor core has the other accumulator's
-// products to run meanwhile (8192 x 8192 x 16 heads x 128: 680 us; 720 us with a running maximum
-// and a tile per warpgroup, 485 us without a cap).  A row's largest weight is then rounded to
+// products to run meanwhile (8192 x 8192 x 16 heads x 128: 670 us; 740 us with a running maximum
+// and a tile per warpgroup, 484 us without a cap).  A row's largest weight is then rounded to
 // bf16 like any other, where a running maximum makes it exactly 1: that shows in rows of few
 // keys, which are bound by latency anyway and keep the maximum (the host's rule).
 template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>

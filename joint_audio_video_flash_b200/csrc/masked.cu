@@ -198,19 +198,19 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
 
 // Rows of few keys (per document, on average) have the forms that lose least where one key has
 // most of a row's weight: a running maximum with a cap, and dQ free of out's rounding without
-// one.  Their time is latency, not arithmetic (2 x 1003 keys, 12 heads of 64, causal: forward 42 us
-// with either form, backward 79 to 85 us with it and 75 to 86 us without); at 8192 keys the
-// maximum costs a capped forward call 720 us instead of 680, and the sum would cost a plain
-// backward call what it costs one with a distance bias, 2140 us instead of 1900.
+// one.  Their time is latency, not arithmetic (2 x 1003 keys, 12 heads of 64, causal: 39 and 76
+// us, the same either way); at 8192 keys the maximum costs a capped forward call 740 us instead
+// of 670, and the sum would cost a plain backward call what it costs one with a distance bias,
+// 2130 us instead of 1900.
 constexpr int kFewKeys = 2048;
 bool few_keys(const ltx::MaskedShape& s) { return s.kv_len / std::max(s.docs, 1) <= kFewKeys; }
 
 // Where a document's queries or keys are one tile (on average), sums have too few terms for the
 // roundings of P and dS to average out, and the backward kernels multiply what the roundings take
 // off as well: relative to the gradients' norm, 2.9e-3 becomes 1.7e-3 (the result's own rounding)
-// at 16 x 16 tokens, for 10 to 15 % of time that is mostly latency (2 x 126 x 15360 x 32 x 64: 404
-// us without, 470 us with it; 2 x 252 in documents of 124: 18.6 us and 20.4 us).  Longer walks
-// would pay 6 products instead of 4 and have 2.4e-3 anyway.
+// at 16 x 16 tokens, for 10 to 16 % of time that is mostly latency (2 x 252 in documents of 124,
+// 2 x 126 x 15360 x 32 x 64).  Longer walks would pay 6 products instead of 4 and have 2.4e-3
+// anyway.
 constexpr int kFineRows = 128;
 bool fine(const ltx::MaskedShape& s) {
   return std::min(s.q_len, s.kv_len) / std::max(s.docs, 1) <= kFineRows;
