@@ -539,8 +539,9 @@ typedef struct ltxattn_masked_grad {
  *     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i
  * summed over the query heads of a key head.  `call` as given to the forward call, out and lse
  * as it wrote them (lse required); the slopes get no gradient.  Queries that see no key have
- * gradient 0, keys that no query sees too; rows of no document are left as they were.  dq, dk
- * and dv must share no byte with each other, with a tensor of `call` or d_out.
+ * gradient 0, keys that no query sees too; a query that sees one key has dq 0, whatever the
+ * score.  Rows of no document are left as they were.  dq, dk and dv must share no byte with
+ * each other, with a tensor of `call` or d_out.
  *
  *   workspace  device, 16-byte aligned, at least what ltxattn_masked_workspace(call, 1) says;
  *              calls that may overlap in time need one each.

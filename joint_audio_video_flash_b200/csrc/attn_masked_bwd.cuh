@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
                         p.d1 + b * p.stride1[0] + m.k0 * p.stride1[1] + hk * p.stride1[2],
                         p.stride1[1], p.parts > 1 ? p.part1 + slab * D : nullptr);
       else
-        masked_store<D>(trow + L::kColK, n > 0, p.scale, smem + L::kDo, j0, m.nk,
+        // a document's only key has all the weight of every query: no score has a gradient
+        masked_store<D>(trow + L::kColK, n > 0, m.nk == 1 ? 0.0f : p.scale, smem + L::kDo, j0, m.nk,
                         p.d0 + b * p.stride0[0] + m.k0 * p.stride0[1] + hk * p.stride0[2],
                         p.stride0[1], p.parts > 1 ? p.part0 + slab * D : nullptr);
     }
@@ -999,6 +1000,10 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
     if (ok) {
       tc_fence_after();
       e += g == 0 ? sums[row] : 0.0f;
+      // A query that sees one key gives it weight 1 whatever the score is: its dQ is 0, where the
+      // two sums would leave the roundings of dS and of P b (1e-8 of N(0, 1) inputs).  e stays:
+      // it brings delta + e to the key's dP, and dS of the other kernel to 0.
+      const float scale = lim == 1 ? 0.0f : p.scale;
       const size_t rows0 =
           (((size_t)part * p.s.batch + b) * p.s.heads + h) * (size_t)p.s.q_len + m.q0;
       __nv_bfloat16* out = p.d0 + b * p.stride0[0] + m.q0 * p.stride0[1] + h * p.stride0[2];
@@ -1009,15 +1014,15 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
             p.part_e[rows0 + i] = e;
             if (part == 0) p.stat[stat_at] = st;
           }
-          masked_store<D>(trow + L::kColQ, n > 0, p.scale, smem + L::kQ, i0, m.nq, out,
+          masked_store<D>(trow + L::kColQ, n > 0, scale, smem + L::kQ, i0, m.nq, out,
                           p.stride0[1], p.part0 + rows0 * D);
         } else if (kFix) {
-          masked_store<D>(trow + L::kColPk, n > 0, p.scale, smem + L::kQ, i0, m.nq, out,
+          masked_store<D>(trow + L::kColPk, n > 0, scale, smem + L::kQ, i0, m.nq, out,
                           p.stride0[1], p.part1 + rows0 * D);
         }
       } else if (g == 0) {
         if (i < m.nq) p.stat[stat_at] = make_float2(st.x, st.y + e);
-        masked_store<D>(trow + L::kColQ, n > 0, p.scale, smem + L::kQ, i0, m.nq, out,
+        masked_store<D>(trow + L::kColQ, n > 0, scale, smem + L::kQ, i0, m.nq, out,
                         p.stride0[1], nullptr, kFix ? trow + L::kColPk : 0u, e);
       }
     }
