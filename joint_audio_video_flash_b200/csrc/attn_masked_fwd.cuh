@@ -901,7 +901,15 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
 
 // Merge of the key parts: L = max lse_p, w_p = 2^(lse_p - L), out = sum w_p o_p / sum w_p.
 // One thread per 4 channels of a row; rows of no document are left as they are.
+// A part whose scores were not finite has lse_p = NaN, which the maximum keeps (fmaxf would drop
+// it): the row is NaN then, as it is without parts, and not the 0 of a row that sees no key.
 constexpr int kMaskedMergeBatch = 8;  // parts whose loads are in flight together
+
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
@@ -936,7 +944,7 @@ __global__ void __launch_bounds__(kCombineThreads)
       }
     }
 #pragma unroll
-    for (int x = 0; x < kMaskedMergeBatch; ++x) next = fmaxf(next, l[x]);
+    for (int x = 0; x < kMaskedMergeBatch; ++x) next = max_or_nan(next, l[x]);
     if (next == -INFINITY) continue;  // nothing seen yet
     const float f = top == -INFINITY ? 0.0f : ex2(top - next);
     top = next;
