@@ -314,6 +314,9 @@ __global__ void __launch_bounds__(kMaskedThreads, 1)
   const MaskedDoc m = *shared_doc;
   const uint32_t tmem = *tmem_slot;
   if (m.tile < 0) {
+    // a grid without a unit (documents of no key) still ends behind the dQ kernel's: what follows
+    // in the stream waits for this grid alone
+    grid_dependency_wait();
     if (warp == 1) tmem_dealloc(tmem, L::kTmemCols);
     return;
   }

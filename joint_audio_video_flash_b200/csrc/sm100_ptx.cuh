@@ -613,8 +613,11 @@ __device__ __forceinline__ void cp_async_wait() {
 // programmatic dependent launch
 // ----------------------------------------------------------------------------
 // Waits until the grids this one depends on are complete and their writes visible; a no-op in
-// a kernel that was launched without the attribute.  Every thread of a dependent kernel calls
-// it ahead of its first access to global memory.
+// a kernel that was launched without the attribute.  Two rules for a dependent kernel: a thread
+// touches what those grids write, or writes what they touch, only behind the wait (what earlier
+// grids of the stream wrote may be read ahead of it when the one before was launched without the
+// attribute or waits itself before it lets its dependents start); and at least one thread of
+// every CTA waits, or the grid could end before them and what comes next in the stream start.
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
