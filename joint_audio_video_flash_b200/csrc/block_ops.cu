@@ -54,11 +54,11 @@ bool views_apart(const View& a, const View& b) {
   return off >= wa && off + wb <= bytes;
 }
 
-template <typename T, bool kHalves>
+template <typename T, bool kHalves, bool kKeep>
 int launch_rope(ltx::RopeParams& p, cudaStream_t stream) {
   using L = ltx::RopeShape<T, kHalves>;
   const int resident =
-      ltx::resident_ctas<ltx::ltx_rope_axes<T, kHalves>>(ltx::kRopeThreads, L::kSmem);
+      ltx::resident_ctas<ltx::ltx_rope_axes<T, kHalves, kKeep>>(ltx::kRopeThreads, L::kSmem);
   if (resident < 1) return LTXATTN_ERR_CUDA;
   p.units = p.head_dim / (L::kParts * L::V);
   const int slots = ltx::kRopeThreads / p.units;  // units <= 128
@@ -69,13 +69,15 @@ int launch_rope(ltx::RopeParams& p, cudaStream_t stream) {
   const long long rows = (long long)p.batch * p.len;
   const unsigned grid =
       (unsigned)std::min<long long>((rows + p.tokens - 1) / p.tokens, resident);
-  ltx::ltx_rope_axes<T, kHalves><<<grid, ltx::kRopeThreads, L::kSmem, stream>>>(p);
+  ltx::ltx_rope_axes<T, kHalves, kKeep><<<grid, ltx::kRopeThreads, L::kSmem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
 }
 
 template <typename T>
 int launch_rope(ltx::RopeParams& p, bool halves, cudaStream_t stream) {
-  return halves ? launch_rope<T, true>(p, stream) : launch_rope<T, false>(p, stream);
+  if (2 * p.pairs < p.head_dim)
+    return halves ? launch_rope<T, true, true>(p, stream) : launch_rope<T, false, true>(p, stream);
+  return halves ? launch_rope<T, true, false>(p, stream) : launch_rope<T, false, false>(p, stream);
 }
 
 // ---------------------------------------------------------------- layer norm
