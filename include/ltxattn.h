@@ -88,7 +88,8 @@ typedef enum {
 /*
  * Creates the context for the CUDA device current on the calling thread:
  * device properties, a zeroed device status word and the kernels' shared-memory
- * limits.  Idempotent: a second call on the same device returns LTXATTN_OK.
+ * limits (the masked calls' kernels are set up by their first calls).  Idempotent: a second
+ * call on the same device returns LTXATTN_OK.
  * Errors: LTXATTN_ERR_CUDA (no device, allocation or attribute failure).
  */
 LTXATTN_API int ltxattn_create(void);

@@ -48,6 +48,7 @@ struct Context {
   int num_sms = 0;
   int* d_status = nullptr;
   EncodeTiledFn encode = nullptr;
+  std::atomic<uint64_t> masked_limits{0};
   std::map<cudaStream_t, Workspace> workspaces;
   // held from a split call's workspace lookup through its launches: a grow on one host
   // thread (stream-ordered free of the old buffer, then a new one) can neither free a
@@ -620,7 +621,6 @@ cudaError_t set_smem_limits_all() {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(ltx::ltx_attn_fwd_a2v, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              ltx::A2vSmem::kAlloc);
-  if (e == cudaSuccess) e = ltx::masked_set_smem_limits();
   return e;
 }
 
@@ -705,9 +705,9 @@ namespace ltx {
 
 int device_context(DeviceContext* out) {
   int st = LTXATTN_OK;
-  const Context* c = current_context(&st);
+  Context* c = current_context(&st);
   if (!c) return st;
-  *out = DeviceContext{c->encode, c->num_sms, c->d_status};
+  *out = DeviceContext{c->encode, c->num_sms, c->d_status, &c->masked_limits};
   return LTXATTN_OK;
 }
 

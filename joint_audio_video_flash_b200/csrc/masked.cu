@@ -1,6 +1,7 @@
 // masked.cu -- host side of attention with masked, capped and distance-biased scores: checks,
 // tensor maps, the plan and the launches of attn_masked_fwd.cuh and attn_masked_bwd.cuh.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "attn_masked_bwd.cuh"
@@ -292,41 +293,79 @@ size_t partial_bytes(const ltx::MaskedShape& s, int head_dim, int parts) {
   return parts > 1 ? (size_t)parts * s.batch * s.heads * s.q_len * (head_dim + 1) * 4 : 0;
 }
 
+// Where a kernel is launched, and which kernels have their limit there.
+struct Launch {
+  cudaStream_t stream;
+  std::atomic<uint64_t>* limits;
+};
+
+// Raises a kernel's limit of dynamic shared memory ahead of its first launch in a context.  Not
+// in ltxattn_create, nor in the allocation-free call's set-up: setting a limit loads the kernel,
+// and with these 58 either took 40 to 50 ms instead of 9 and 6 MB more of device memory, of
+// callers that never use them too.
+template <int kIndex>
+cudaError_t raise_limit(const void* kernel, int bytes, const Launch& on) {
+  static_assert(kIndex >= 0 && kIndex < 64, "a bit of one word each");
+  constexpr uint64_t kBit = 1ull << kIndex;
+  if (on.limits->load(std::memory_order_acquire) & kBit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) on.limits->fetch_or(kBit, std::memory_order_release);
+  return e;
+}
+
+// The kernels' numbers: 24 of the forward call, then 17 of the backward call per head_dim.
+constexpr int fwd_index(int d, bool alt, bool cap, bool bias, bool fixed) {
+  return ((d == 128) * 2 + alt) * 6 + (cap ? 2 + fixed * 2 : 0) + bias;
+}
+constexpr int bwd_index(int d, bool of_q, bool cap, bool bias, bool fix, bool fine) {
+  return 24 + (d == 128) * 17 + (!of_q ? cap * 4 + bias * 2 + fine
+                                 : fix ? 8 + cap * 4 + bias * 2 + fine
+                                       : 16);
+}
+static_assert(fwd_index(128, true, true, true, true) == 23 &&
+                  bwd_index(64, false, false, false, false, false) == 24 &&
+                  bwd_index(128, true, false, false, false, false) == 57,
+              "no number twice");
+
 template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>
 cudaError_t launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                       const ltx::MaskedFwdParams& p, int units, cudaStream_t stream) {
+                       const ltx::MaskedFwdParams& p, int units, const Launch& on) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.tile_heads, p.s.batch, p.parts);
-  ltx::ltx_masked_fwd<D, kAlt, kCap, kBias, kFixed>
-      <<<grid, ltx::kMaskedThreads, ltx::MaskedSmem<D, kAlt>::kAlloc, stream>>>(tq, tk, tv, p);
+  const auto kernel = ltx::ltx_masked_fwd<D, kAlt, kCap, kBias, kFixed>;
+  constexpr int kSmem = ltx::MaskedSmem<D, kAlt>::kAlloc;
+  const cudaError_t e = raise_limit<fwd_index(D, kAlt, kCap, kBias, kFixed)>(
+      reinterpret_cast<const void*>(kernel), kSmem, on);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, ltx::kMaskedThreads, kSmem, on.stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 
 template <int D, bool kAlt>
 cudaError_t launch_fwd_scores(bool cap, bool bias, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const ltx::MaskedFwdParams& p, int units,
-                              cudaStream_t stream) {
+                              const Launch& on) {
   if (cap && p.s.cap_log2 <= ltx::kFixedMaxCap && !few_keys(p.s) && !fine(p.s))
-    return bias ? launch_fwd<D, kAlt, true, true, true>(tq, tk, tv, p, units, stream)
-                : launch_fwd<D, kAlt, true, false, true>(tq, tk, tv, p, units, stream);
+    return bias ? launch_fwd<D, kAlt, true, true, true>(tq, tk, tv, p, units, on)
+                : launch_fwd<D, kAlt, true, false, true>(tq, tk, tv, p, units, on);
   if (cap)
-    return bias ? launch_fwd<D, kAlt, true, true, false>(tq, tk, tv, p, units, stream)
-                : launch_fwd<D, kAlt, true, false, false>(tq, tk, tv, p, units, stream);
-  return bias ? launch_fwd<D, kAlt, false, true, false>(tq, tk, tv, p, units, stream)
-              : launch_fwd<D, kAlt, false, false, false>(tq, tk, tv, p, units, stream);
+    return bias ? launch_fwd<D, kAlt, true, true, false>(tq, tk, tv, p, units, on)
+                : launch_fwd<D, kAlt, true, false, false>(tq, tk, tv, p, units, on);
+  return bias ? launch_fwd<D, kAlt, false, true, false>(tq, tk, tv, p, units, on)
+              : launch_fwd<D, kAlt, false, false, false>(tq, tk, tv, p, units, on);
 }
 
 template <int D>
 cudaError_t launch_forward(const FwdPlan& f, bool cap, bool bias, const CUtensorMap& tq,
                            const CUtensorMap& tk, const CUtensorMap& tv,
-                           const ltx::MaskedFwdParams& p, cudaStream_t stream) {
-  cudaError_t e = f.alt
-                      ? launch_fwd_scores<D, true>(cap, bias, tq, tk, tv, p, f.units, stream)
-                      : launch_fwd_scores<D, false>(cap, bias, tq, tk, tv, p, f.units, stream);
+                           const ltx::MaskedFwdParams& p, const Launch& on) {
+  cudaError_t e = f.alt ? launch_fwd_scores<D, true>(cap, bias, tq, tk, tv, p, f.units, on)
+                        : launch_fwd_scores<D, false>(cap, bias, tq, tk, tv, p, f.units, on);
   if (e == cudaSuccess && p.parts > 1) {
     const long long n = (long long)p.s.batch * p.s.heads * p.s.q_len * (D / 4);
     e = ltx::launch_dependent(ltx::ltx_masked_combine<D>,
                               (unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads),
-                              ltx::kCombineThreads, 0, stream, p);
+                              ltx::kCombineThreads, 0, on.stream, p);
   }
   return e;
 }
@@ -373,53 +412,60 @@ struct BwdMaps {
 
 template <int D, bool kCap, bool kBias, bool kFine>
 cudaError_t launch_kv(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
-                      cudaStream_t stream) {
+                      const Launch& on) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.kv_heads, p.s.batch, p.parts);
-  return ltx::launch_dependent(ltx::ltx_masked_bwd_kv<D, kCap, kBias, kFine>, grid,
-                               ltx::kMaskedThreads, ltx::BwdKvSmem<D>::kAlloc, stream, t.q, t.k,
-                               t.v, t.d_out, p);
+  const auto kernel = ltx::ltx_masked_bwd_kv<D, kCap, kBias, kFine>;
+  constexpr int kSmem = ltx::BwdKvSmem<D>::kAlloc;
+  const cudaError_t e = raise_limit<bwd_index(D, false, kCap, kBias, false, kFine)>(
+      reinterpret_cast<const void*>(kernel), kSmem, on);
+  if (e != cudaSuccess) return e;
+  return ltx::launch_dependent(kernel, grid, ltx::kMaskedThreads, kSmem, on.stream, t.q, t.k, t.v,
+                               t.d_out, p);
 }
 
 template <int D, bool kCap, bool kBias, bool kFix, bool kFine>
 cudaError_t launch_q(const BwdMaps& t, const ltx::MaskedBwdParams& p, int units,
-                     cudaStream_t stream) {
+                     const Launch& on) {
   const unsigned grid = (unsigned)grid_ctas(units, p.s.heads, p.s.batch, p.parts);
-  ltx::ltx_masked_bwd_q<D, kCap, kBias, kFix, kFine>
-      <<<grid, ltx::kMaskedThreads, ltx::BwdQSmem<D, kFix>::kAlloc, stream>>>(t.q, t.k, t.v,
-                                                                              t.d_out, p);
+  const auto kernel = ltx::ltx_masked_bwd_q<D, kCap, kBias, kFix, kFine>;
+  constexpr int kSmem = ltx::BwdQSmem<D, kFix>::kAlloc;
+  const cudaError_t e = raise_limit<bwd_index(D, true, kCap, kBias, kFix, kFine)>(
+      reinterpret_cast<const void*>(kernel), kSmem, on);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, ltx::kMaskedThreads, kSmem, on.stream>>>(t.q, t.k, t.v, t.d_out, p);
   return cudaGetLastError();
 }
 
 template <int D, bool kCap, bool kBias>
 cudaError_t launch_both(bool of_q, bool fine, bool fix, const BwdMaps& t,
-                        const ltx::MaskedBwdParams& p, int units, cudaStream_t stream) {
+                        const ltx::MaskedBwdParams& p, int units, const Launch& on) {
   if (!of_q)
-    return fine ? launch_kv<D, kCap, kBias, true>(t, p, units, stream)
-                : launch_kv<D, kCap, kBias, false>(t, p, units, stream);
-  if (fine) return launch_q<D, kCap, kBias, true, true>(t, p, units, stream);
+    return fine ? launch_kv<D, kCap, kBias, true>(t, p, units, on)
+                : launch_kv<D, kCap, kBias, false>(t, p, units, on);
+  if (fine) return launch_q<D, kCap, kBias, true, true>(t, p, units, on);
   if constexpr (!kCap && !kBias)
-    if (!fix) return launch_q<D, false, false, false, false>(t, p, units, stream);
-  return launch_q<D, kCap, kBias, true, false>(t, p, units, stream);
+    if (!fix) return launch_q<D, false, false, false, false>(t, p, units, on);
+  return launch_q<D, kCap, kBias, true, false>(t, p, units, on);
 }
 
 template <int D>
 cudaError_t launch_scores(bool of_q, bool cap, bool fine, bool fix, const BwdMaps& t,
-                          const ltx::MaskedBwdParams& p, int units, cudaStream_t stream) {
+                          const ltx::MaskedBwdParams& p, int units, const Launch& on) {
   const bool bias = p.s.slopes != nullptr;
-  return cap ? (bias ? launch_both<D, true, true>(of_q, fine, fix, t, p, units, stream)
-                     : launch_both<D, true, false>(of_q, fine, fix, t, p, units, stream))
-             : (bias ? launch_both<D, false, true>(of_q, fine, fix, t, p, units, stream)
-                     : launch_both<D, false, false>(of_q, fine, fix, t, p, units, stream));
+  return cap ? (bias ? launch_both<D, true, true>(of_q, fine, fix, t, p, units, on)
+                     : launch_both<D, true, false>(of_q, fine, fix, t, p, units, on))
+             : (bias ? launch_both<D, false, true>(of_q, fine, fix, t, p, units, on)
+                     : launch_both<D, false, false>(of_q, fine, fix, t, p, units, on));
 }
 
 template <int D, bool kDq>
-cudaError_t launch_sum(const ltx::MaskedBwdParams& p, cudaStream_t stream) {
+cudaError_t launch_sum(const ltx::MaskedBwdParams& p, const Launch& on) {
   const long long rows = kDq ? (long long)p.s.batch * p.s.heads * p.s.q_len
                              : 2LL * p.s.batch * p.s.kv_heads * p.s.kv_len;
   const long long n = rows * (D / 4);
   return ltx::launch_dependent(ltx::ltx_masked_bwd_sum<D, kDq>,
                                (unsigned)((n + ltx::kCombineThreads - 1) / ltx::kCombineThreads),
-                               ltx::kCombineThreads, 0, stream, p);
+                               ltx::kCombineThreads, 0, on.stream, p);
 }
 
 void set_target(const Tensor& t, __nv_bfloat16** base, long long* stride) {
@@ -433,7 +479,7 @@ template <int D>
 cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, const Tensors& t,
                             const Tensor& d_out, const Tensor& dq, const Tensor& dk,
                             const Tensor& dv, const BwdMaps& maps, ltx::MaskedBwdParams p,
-                            float* partials, cudaStream_t stream) {
+                            float* partials, const Launch& on) {
   __nv_bfloat16* base;
   set_target(t.out, &base, p.out_stride);
   p.out = base;
@@ -450,9 +496,9 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
     p.part1 = fix ? partials + rows * D : nullptr;
     p.part_e = partials + rows * D * (fix ? 2 : 1);
   }
-  cudaError_t e = launch_scores<D>(true, cap, fine(p.s), fix, maps, p, f.units_q, stream);
+  cudaError_t e = launch_scores<D>(true, cap, fine(p.s), fix, maps, p, f.units_q, on);
   if (e == cudaSuccess && p.parts > 1)
-    e = launch_sum<D, true>(p, stream);
+    e = launch_sum<D, true>(p, on);
   if (e != cudaSuccess) return e;
   // dK and dV
   p.parts = f.parts_kv;
@@ -463,71 +509,12 @@ cudaError_t launch_backward(const BwdPlan& f, const ltxattn_masked_call& a, cons
     p.part0 = partials;
     p.part1 = partials + (size_t)p.parts * a.batch * a.kv_heads * a.kv_len * D;
   }
-  e = launch_scores<D>(false, cap, fine(p.s), fix, maps, p, f.units_kv, stream);
-  if (e == cudaSuccess && p.parts > 1) e = launch_sum<D, false>(p, stream);
-  return e;
-}
-
-template <int D, bool kCap, bool kBias, bool kFine>
-cudaError_t set_bwd() {
-  cudaError_t e = cudaFuncSetAttribute(ltx::ltx_masked_bwd_kv<D, kCap, kBias, kFine>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       ltx::BwdKvSmem<D>::kAlloc);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, kCap, kBias, true, kFine>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ltx::BwdQSmem<D, true>::kAlloc);
-}
-
-template <int D>
-cudaError_t set_bwd_scores() {
-  cudaError_t e = cudaFuncSetAttribute(ltx::ltx_masked_bwd_q<D, false, false, false, false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       ltx::BwdQSmem<D, false>::kAlloc);
-  if (e == cudaSuccess) e = set_bwd<D, false, false, false>();
-  if (e == cudaSuccess) e = set_bwd<D, false, false, true>();
-  if (e == cudaSuccess) e = set_bwd<D, false, true, false>();
-  if (e == cudaSuccess) e = set_bwd<D, false, true, true>();
-  if (e == cudaSuccess) e = set_bwd<D, true, false, false>();
-  if (e == cudaSuccess) e = set_bwd<D, true, false, true>();
-  if (e == cudaSuccess) e = set_bwd<D, true, true, false>();
-  if (e == cudaSuccess) e = set_bwd<D, true, true, true>();
-  return e;
-}
-
-template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>
-cudaError_t set_fwd() {
-  return cudaFuncSetAttribute(ltx::ltx_masked_fwd<D, kAlt, kCap, kBias, kFixed>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ltx::MaskedSmem<D, kAlt>::kAlloc);
-}
-
-template <int D, bool kAlt>
-cudaError_t set_fwd_scores() {
-  cudaError_t e = set_fwd<D, kAlt, false, false, false>();
-  if (e == cudaSuccess) e = set_fwd<D, kAlt, false, true, false>();
-  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, false, false>();
-  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, true, false>();
-  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, false, true>();
-  if (e == cudaSuccess) e = set_fwd<D, kAlt, true, true, true>();
+  e = launch_scores<D>(false, cap, fine(p.s), fix, maps, p, f.units_kv, on);
+  if (e == cudaSuccess && p.parts > 1) e = launch_sum<D, false>(p, on);
   return e;
 }
 
 }  // namespace
-
-namespace ltx {
-
-cudaError_t masked_set_smem_limits() {
-  cudaError_t e = set_fwd_scores<64, false>();
-  if (e == cudaSuccess) e = set_fwd_scores<64, true>();
-  if (e == cudaSuccess) e = set_fwd_scores<128, false>();
-  if (e == cudaSuccess) e = set_fwd_scores<128, true>();
-  if (e == cudaSuccess) e = set_bwd_scores<64>();
-  if (e == cudaSuccess) e = set_bwd_scores<128>();
-  return e;
-}
-
-}  // namespace ltx
 
 extern "C" {
 
@@ -596,11 +583,11 @@ int ltxattn_masked_forward(const ltxattn_masked_call* call, void* workspace,
   if (!encode(c, &tq, t.q, ltx::kBlockM / p.s.pack, p.s.pack) ||
       !encode(c, &tk, t.k, ltx::kBlockN, 1) || !encode(c, &tv, t.v, ltx::kBlockN, 1))
     return LTXATTN_ERR_CUDA;
-  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const Launch on{reinterpret_cast<cudaStream_t>(stream_), c.masked_limits};
   const bool cap = a.softcap > 0.0f, bias = a.slopes != nullptr;
   const cudaError_t e = a.head_dim == 64
-                            ? launch_forward<64>(f, cap, bias, tq, tk, tv, p, stream)
-                            : launch_forward<128>(f, cap, bias, tq, tk, tv, p, stream);
+                            ? launch_forward<64>(f, cap, bias, tq, tk, tv, p, on)
+                            : launch_forward<128>(f, cap, bias, tq, tk, tv, p, on);
   return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
 }
 
@@ -665,10 +652,10 @@ int ltxattn_masked_backward(const ltxattn_masked_call* call, const ltxattn_maske
   if (!encode(c, &maps.q, t.q, ltx::kBlockM, 1) || !encode(c, &maps.k, t.k, ltx::kBlockN, 1) ||
       !encode(c, &maps.v, t.v, ltx::kBlockN, 1) || !encode(c, &maps.d_out, d_out, ltx::kBlockM, 1))
     return LTXATTN_ERR_CUDA;
-  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const Launch on{reinterpret_cast<cudaStream_t>(stream_), c.masked_limits};
   const cudaError_t e =
-      d == 64 ? launch_backward<64>(f, a, t, d_out, dq, dk, dv, maps, p, partials, stream)
-              : launch_backward<128>(f, a, t, d_out, dq, dk, dv, maps, p, partials, stream);
+      d == 64 ? launch_backward<64>(f, a, t, d_out, dq, dk, dv, maps, p, partials, on)
+              : launch_backward<128>(f, a, t, d_out, dq, dk, dv, maps, p, partials, on);
   return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
 }
 
