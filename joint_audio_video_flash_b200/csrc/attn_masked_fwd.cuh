@@ -13,7 +13,8 @@
 // a row's last tiles pay for the comparison.
 //
 // Tiles start at a document's first query, so a tile holds rows of one document.  The document
-// offsets live on the device; a CTA finds its (document, tile) by a warp scan over them.
+// offsets live on the device; a CTA finds its (document, tile) by a warp scan over 32 of them,
+// or by a search among more.
 // Query heads that share a key head are packed into the rows of a tile (row = token * pack +
 // head, pack = heads / kv_heads rounded up to a power of two): one pass over K and V serves
 // all of them, which is what bounds single-token queries (2 x 1 x 27280 x 40 heads over 8 x 128:
@@ -117,10 +118,43 @@ __device__ __forceinline__ MaskedPlace masked_place(int heads, int batch, int pa
   return w;
 }
 
+// Up to so many documents are taken in the order of their work.
+constexpr int kMaxSortedDocs = 32;
+
+// More than kMaxSortedDocs documents: document d has the units from first / rows + d on (first
+// its first row), which leaves room for the (n + rows - 1) / rows that its n rows make, with one
+// to spare at most, and grows with d.  So a unit's document is found by a search, 32 places a
+// step: at most 4 loads one after the other for 65535 documents, where adding up the units of
+// all the documents ahead, in every CTA, is quadratic in their number.  Measured forwards, adding
+// up and searching: 64 documents of 64 tokens, 8 heads of 64, 52 and 55 us; 1024 of them 1.34 and
+// 0.41 ms; 65535 of one token, one head, 369 and 2.9 ms.
+__host__ __device__ __forceinline__ int masked_first_unit(int first, int d, int rows) {
+  return first / rows + d;
+}
+
+// The last document whose units begin at `unit` or ahead of it; -1: none does.  Whole warp.
+__device__ __forceinline__ int masked_search(const int* starts, int docs, int len, int unit,
+                                             int rows) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, span = docs;
+  for (;;) {
+    const int step = (span + 31) / 32, d = lo + lane * step;
+    bool ahead = false;
+    if (lane * step < span)
+      ahead = masked_first_unit(min(max(__ldg(starts + d), 0), len), d, rows) <= unit;
+    const uint32_t found = __ballot_sync(0xffffffffu, ahead);
+    if (!found) return -1;  // in the first step, where lane 0 looks at document 0
+    const int at = (31 - __clz(found)) * step;
+    lo += at;
+    span = min(span - at, step);
+    if (step == 1) return lo;
+  }
+}
+
 // Unit `unit` of batch row b when every document is cut into units of `rows` rows of its
-// queries (kKeys: of its keys).  Up to 32 documents are taken in the order of their units'
-// work (the other axis's length), the longest first, more in their own order; within a causal
-// document the later queries, which see more, come first.  Whole warp.
+// queries (kKeys: of its keys).  Up to kMaxSortedDocs documents are taken in the order of their
+// units' work (the other axis's length), the longest first, more in their own order; within a
+// causal document the later queries, which see more, come first.  Whole warp.
 template <bool kKeys>
 __device__ __forceinline__ MaskedDoc masked_find(const MaskedShape& s, int b, int unit,
                                                  int rows) {
@@ -139,35 +173,40 @@ __device__ __forceinline__ MaskedDoc masked_find(const MaskedShape& s, int b, in
   }
   const int* qs = s.q_starts + (size_t)b * (s.docs + 1);
   const int* ks = s.kv_starts + (size_t)b * (s.docs + 1);
-  for (int d0 = 0; d0 < s.docs; d0 += 32) {
-    const int d = d0 + lane;
-    int q0 = 0, nq = 0, k0 = 0, nk = 0, prefix = 0;
-    if (d < s.docs) {
-      masked_range(qs, d, s.q_len, q0, nq);
-      masked_range(ks, d, s.kv_len, k0, nk);
-      if (s.prefix) prefix = __ldg(s.prefix + (size_t)b * s.docs + d);
-    }
-    const int tiles = ((kKeys ? nk : nq) + rows - 1) / rows;
-    const int weight = s.docs <= 32 ? (kKeys ? nq : nk) : 0;
-    const int here = min(s.docs - d0, 32);
-    int end = 0;  // units up to and with this document's
-    for (int x = 0; x < here; ++x) {
-      const int wx = __shfl_sync(0xffffffffu, weight, x), tx = __shfl_sync(0xffffffffu, tiles, x);
-      if (wx > weight || (wx == weight && x <= lane)) end += tx;
-    }
-    const uint32_t hit =
-        __ballot_sync(0xffffffffu, lane < here && end - tiles <= unit && unit < end);
-    if (hit) {
-      const int at = __ffs(hit) - 1;
-      m.q0 = __shfl_sync(0xffffffffu, q0, at);
-      m.nq = __shfl_sync(0xffffffffu, nq, at);
-      m.k0 = __shfl_sync(0xffffffffu, k0, at);
-      m.nk = __shfl_sync(0xffffffffu, nk, at);
-      m.prefix = __shfl_sync(0xffffffffu, prefix, at);
-      m.tile = __shfl_sync(0xffffffffu, nth(unit - (end - tiles), tiles), at);
-      return m;
-    }
-    unit -= __reduce_add_sync(0xffffffffu, tiles);
+  if (s.docs > kMaxSortedDocs) {
+    const int d = masked_search(kKeys ? ks : qs, s.docs, kKeys ? s.kv_len : s.q_len, unit, rows);
+    if (d < 0) return m;
+    masked_range(qs, d, s.q_len, m.q0, m.nq);
+    masked_range(ks, d, s.kv_len, m.k0, m.nk);
+    m.prefix = s.prefix ? __ldg(s.prefix + (size_t)b * s.docs + d) : 0;
+    const int n = unit - masked_first_unit(kKeys ? m.k0 : m.q0, d, rows);
+    const int tiles = ((kKeys ? m.nk : m.nq) + rows - 1) / rows;
+    if (n < tiles) m.tile = nth(n, tiles);
+    return m;
+  }
+  int q0 = 0, nq = 0, k0 = 0, nk = 0, prefix = 0;
+  if (lane < s.docs) {
+    masked_range(qs, lane, s.q_len, q0, nq);
+    masked_range(ks, lane, s.kv_len, k0, nk);
+    if (s.prefix) prefix = __ldg(s.prefix + (size_t)b * s.docs + lane);
+  }
+  const int tiles = ((kKeys ? nk : nq) + rows - 1) / rows;
+  const int weight = kKeys ? nq : nk;
+  int end = 0;  // units up to and with this document's
+  for (int x = 0; x < s.docs; ++x) {
+    const int wx = __shfl_sync(0xffffffffu, weight, x), tx = __shfl_sync(0xffffffffu, tiles, x);
+    if (wx > weight || (wx == weight && x <= lane)) end += tx;
+  }
+  const uint32_t hit =
+      __ballot_sync(0xffffffffu, lane < s.docs && end - tiles <= unit && unit < end);
+  if (hit) {
+    const int at = __ffs(hit) - 1;
+    m.q0 = __shfl_sync(0xffffffffu, q0, at);
+    m.nq = __shfl_sync(0xffffffffu, nq, at);
+    m.k0 = __shfl_sync(0xffffffffu, k0, at);
+    m.nk = __shfl_sync(0xffffffffu, nk, at);
+    m.prefix = __shfl_sync(0xffffffffu, prefix, at);
+    m.tile = __shfl_sync(0xffffffffu, nth(unit - (end - tiles), tiles), at);
   }
   return m;
 }

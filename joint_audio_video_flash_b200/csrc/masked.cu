@@ -228,8 +228,10 @@ struct FwdPlan {
 };
 
 // Most units of `rows` rows that `docs` documents (0: one) of `len` rows in all can have: a
-// document of n rows has (n + rows - 1) / rows at most.
+// document of n rows has (n + rows - 1) / rows at most, and their numbers have gaps where there
+// are many (masked_find).
 int max_units(int len, int docs, int rows) {
+  if (docs > ltx::kMaxSortedDocs) return ltx::masked_first_unit(len, docs, rows);
   return (int)((len + (long long)std::max(docs, 1) * (rows - 1)) / rows);
 }
 
