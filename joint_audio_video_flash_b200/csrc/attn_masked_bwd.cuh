@@ -14,8 +14,9 @@
 // K_j (b the cap's derivative).  With kFix the kernel carries that sum as a second accumulator
 // and takes it out.  The host asks for it with a cap (which is there because scores are large;
 // the softmax's arithmetic bounds the kernel then, and the product is nearly free), with a bias
-// (which gathers the weight on the near keys) and for rows of few keys.  For long rows of plain
-// scores it would add a third to the kernel's bound for an error that does not show: measured
+// (which gathers the weight on the near keys) and where documents have few keys on average; the
+// early rows of a long causal document of plain scores go without.  For long rows of plain scores
+// it would add a third to the kernel's bound for an error that does not show: measured
 // against 64 bits, relative to the gradient's norm, dQ is 2.4e-3 off without it at 7680 keys and
 // N(0, 1) scores, of which 1.7e-3 is the rounding of the result; at 16 keys 2.7e-3 without, and
 // with capped scores of deviation 4 3.6e-3 without and 2.4e-3 with it.

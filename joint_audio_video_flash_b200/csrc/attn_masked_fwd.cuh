@@ -384,7 +384,9 @@ constexpr float kFixedMaxCap = 90.0f;
 // products to run meanwhile (8192 x 8192 x 16 heads x 128: 670 us; 740 us with a running maximum
 // and a tile per warpgroup, 484 us without a cap).  A row's largest weight is then rounded to
 // bf16 like any other, where a running maximum makes it exactly 1: that shows in rows of few
-// keys, which are bound by latency anyway and keep the maximum (the host's rule).
+// keys.  Calls whose documents have few keys on average keep the maximum (the host's rule); the
+// first rows of a long causal document do not, and a row that sees one key gets
+// bf16(2^s) / 2^s times its value there, up to 2^-8 off like every product with P.
 template <int D, bool kAlt, bool kCap, bool kBias, bool kFixed>
 __global__ void __launch_bounds__(kMaskedThreads, 1)
     ltx_masked_fwd(const __grid_constant__ CUtensorMap tm_q,

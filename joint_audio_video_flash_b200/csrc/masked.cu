@@ -197,21 +197,26 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
   return s;
 }
 
-// Rows of few keys (per document, on average) have the forms that lose least where one key has
-// most of a row's weight: a running maximum with a cap, and dQ free of out's rounding without
-// one.  Their time is latency, not arithmetic (2 x 1003 keys, 12 heads of 64, causal: 39 and 76
-// us, the same either way); at 8192 keys the maximum costs a capped forward call 740 us instead
-// of 670, and the sum would cost a plain backward call what it costs one with a distance bias,
-// 2130 us instead of 1900.
+// Calls whose documents have few keys on average have the forms that lose least where one key has
+// most of a row's weight: a running maximum with a cap, and dQ free of out's rounding without one.
+// It is the average that counts, so the early rows of a long causal document, and a short document
+// among long ones, have what the long ones have (their weights and P are rounded to bf16 then, as
+// everybody's).  Measured at head_dim 128, 16 heads, 4096 rows in all; the maximum against none,
+// capped scores of deviation 4 forwards: 1024 keys 76 and 68 us, 2048 keys 127 and 111 us, 8192
+// keys (8192 rows) 780 and 694 us, for 1.7e-3 instead of 2.3e-3 of the result's norm; the sum
+// against none, plain scores backwards: 191 and 178, 299 and 274, 1698 and 1532 us, for 2.36e-3
+// instead of 2.37e-3 (2.40e-3 and 2.43e-3 at 128 keys).  2048 is a choice between the two, not an
+// edge in either.
 constexpr int kFewKeys = 2048;
 bool few_keys(const ltx::MaskedShape& s) { return s.kv_len / std::max(s.docs, 1) <= kFewKeys; }
 
 // Where a document's queries or keys are one tile (on average), sums have too few terms for the
 // roundings of P and dS to average out, and the backward kernels multiply what the roundings take
-// off as well: relative to the gradients' norm, 2.9e-3 becomes 1.7e-3 (the result's own rounding)
-// at 16 x 16 tokens, for 10 to 16 % of time that is mostly latency (2 x 252 in documents of 124,
-// 2 x 126 x 15360 x 32 x 64).  Longer walks would pay 6 products instead of 4 and have 2.4e-3
-// anyway.
+// off as well.  Relative to the gradients' norm, 2.9e-3 becomes 1.7e-3 (the result's own rounding)
+// at 16 x 16 tokens and 2.4e-3 becomes 1.7e-3 from 128 x 128 on.  It costs more the longer the
+// walk is, 6 products instead of 4: 100 against 92 us for a batch of 32 of 128 x 128, 154
+// against 135 us for 8 of 512 x 512, 348 against 299 us for 2 of 2048 x 2048 (16 heads of 128), so
+// longer walks keep the 2.4e-3.
 constexpr int kFineRows = 128;
 bool fine(const ltx::MaskedShape& s) {
   return std::min(s.q_len, s.kv_len) / std::max(s.docs, 1) <= kFineRows;
@@ -380,7 +385,7 @@ struct BwdPlan {
 };
 
 // Whether the dQ kernel carries the sum that takes out's rounding off dQ (attn_masked_bwd.cuh):
-// where scores are capped or biased, or rows have few keys, or P and dS are exact.
+// where scores are capped or biased, or documents have few keys, or P and dS have 16 bits.
 bool dq_fix(const ltx::MaskedShape& s, bool cap) {
   return cap || s.slopes || fine(s) || few_keys(s);
 }
