@@ -182,8 +182,22 @@ struct GradPlan {
   int chunks;  // 2 or 4 a thread; 0: rows too wide, or no common alignment
   NormFit fit;
   int lanes, phases, ctas_per_group;
+  int parts;  // partial dweights and dbiases per group
   size_t workspace;  // bytes of partials
 };
+
+// CTAs along the columns of ltx_layer_norm_grad_cols, and how many of them share a group's rows
+// and write a partial each: kColWaves times what the device holds in all, and no more than one per
+// resident CTA.  The partials are then 7 MB or less at any size; with one per resident CTA whatever
+// the columns are they took 116 MB at 2000 x 16384 bf16 (294 us a call, 164 us now) and 537 MB at
+// 64 x 2^20.  Two waves are as fast with longer chains of additions, one is 8 % slower there.
+constexpr int kColWaves = 4;
+int col_blocks(int cols) { return (cols + ltx::kNormThreads - 1) / ltx::kNormThreads; }
+int col_parts(int resident, int cols, long long groups, long long rows_per_group) {
+  const long long ctas = (long long)col_blocks(cols) * groups;
+  const long long parts = (kColWaves * (long long)resident + ctas - 1) / ctas;
+  return (int)std::min({rows_per_group, parts, std::max<long long>(1, resident / groups)});
+}
 
 template <typename T, int kChunks, NormFit kFit>
 int grad_resident(bool affine) {
@@ -229,8 +243,10 @@ int grad_plan(int cols, const NormLayout& l, bool affine, long long groups,
   }
   if (resident < 1) return LTXATTN_ERR_CUDA;
   plan->ctas_per_group = norm_ctas(resident, groups, rows_per_group, plan->lanes, plan->phases);
-  plan->workspace = affine && plan->ctas_per_group > 1
-                        ? (size_t)groups * plan->ctas_per_group * 2 * cols * sizeof(float)
+  plan->parts = plan->chunks ? plan->ctas_per_group
+                             : col_parts(resident, cols, groups, rows_per_group);
+  plan->workspace = affine && plan->parts > 1
+                        ? (size_t)groups * plan->parts * 2 * cols * sizeof(float)
                         : 0;
   return LTXATTN_OK;
 }
@@ -280,9 +296,11 @@ int layer_norm_grad(const ltx::NormParams& p, long long groups, bool affine,
   } else {
     const unsigned grid = (unsigned)(groups * p.ctas_per_group);
     if (affine) {  // ahead of dx, which may replace x or dy
-      const unsigned blocks =
-          (unsigned)std::min(64, (p.cols + ltx::kNormThreads - 1) / ltx::kNormThreads);
-      ltx::ltx_layer_norm_grad_cols<T><<<dim3(grid, blocks), ltx::kNormThreads, 0, stream>>>(p);
+      ltx::NormParams cols = p;
+      cols.ctas_per_group = plan.parts;
+      ltx::ltx_layer_norm_grad_cols<T>
+          <<<dim3((unsigned)(groups * plan.parts), (unsigned)col_blocks(p.cols)),
+             ltx::kNormThreads, 0, stream>>>(cols);
       e = cudaGetLastError();
     }
     if (e == cudaSuccess) {
@@ -291,10 +309,10 @@ int layer_norm_grad(const ltx::NormParams& p, long long groups, bool affine,
     }
   }
   if (e == cudaSuccess && p.partial) {
-    const int col_blocks = (2 * p.cols + 31) / 32;
-    e = ltx::launch_dependent(ltx::ltx_layer_norm_grad_sum, (unsigned)(groups * col_blocks),
+    const int sum_blocks = (2 * p.cols + 31) / 32;
+    e = ltx::launch_dependent(ltx::ltx_layer_norm_grad_sum, (unsigned)(groups * sum_blocks),
                               ltx::kNormSumWarps * 32, 0, stream, (const float*)p.partial,
-                              p.dweight, p.dbias, p.ctas_per_group, p.cols, col_blocks);
+                              p.dweight, p.dbias, plan.parts, p.cols, sum_blocks);
   }
   return e == cudaSuccess ? LTXATTN_OK : LTXATTN_ERR_CUDA;
 }
