@@ -391,7 +391,8 @@ typedef struct ltxattn_rope_call {
  *                  contiguous (views of a fused projection; head-major tensors).  Each output
  *                  may be its own input (same address and strides) and must otherwise share
  *                  no byte with q, k, the other output or positions: their address ranges are
- *                  apart, or they are parts of the same rows (INVALID_ARG when neither shows)
+ *                  apart, or they are parts of the same rows (INVALID_ARG when neither shows);
+ *                  no two elements of an output lie at one address
  *   head_dim       a multiple of 8 (16 in the halves layout), at most 512; axes <= 4
  *   batch * len    below 2^31
  * Arithmetic in fp32, one rounding at the end.  Needs no ltxattn_create.  Base addresses and
@@ -493,15 +494,17 @@ typedef struct ltxattn_masked_call {
  *     visible: not causal, or j <= p, or j < prefix[b][d]
  *     out_i = sum_j softmax(s)_j v_j,  lse_i = log2 sum_j exp(s_j)
  * Query head h uses key head h / (heads / kv_heads).  A query that sees no key gets out = 0 and
- * lse = -inf.  Rows of no document (ahead of the first offset, behind the last) are not read
- * as queries and their out and lse are left as they were.  Key and value rows outside a
- * document never reach its results, whatever they hold (infinities and NaN included); a value
- * row of the document itself that is not finite may reach every query of the document.
+ * lse = -inf, one that sees a NaN score NaN in both.  Rows of no document (ahead of the first
+ * offset, behind the last) are not read as queries and their out and lse are left as they were.
+ * Key and value rows outside a document never reach its results, whatever they hold (infinities
+ * and NaN included); a value row of the document itself that is not finite may reach every query
+ * of the document.
  *
  *   q, out  bf16 [batch, q_len, heads, head_dim]; k, v bf16 [batch, kv_len, kv_heads,
  *           head_dim]; device, channels contiguous, other strides any positive multiple of
  *           16 bytes.  out must share no byte with q, k, v or a smaller array (address ranges
- *           apart, or parts of the same rows), nor lse with anything.
+ *           apart, or parts of the same rows), nor lse with anything; no two elements of out lie
+ *           at one address.
  *   head_dim 64 or 128; heads % kv_heads == 0; sizes as ltxattn_forward; docs <= 65535
  *   q_starts, kv_starts  not decreasing along a batch row, from 0 to q_len / kv_len.  They are
  *           read on the device; offsets that break this give unspecified values in out and
@@ -542,7 +545,9 @@ typedef struct ltxattn_masked_grad {
  * as it wrote them (lse required); the slopes get no gradient.  Queries that see no key have
  * gradient 0, keys that no query sees too; a query that sees one key has dq 0, whatever the
  * score.  Rows of no document are left as they were.  dq, dk and dv must share no byte with
- * each other, with a tensor of `call` or d_out.
+ * each other, with a tensor of `call` or d_out, and no two elements of one of them lie at one
+ * address.  Rows outside a document never reach its gradients, whatever they hold; a row of the
+ * document itself (of q, k, v, out or d_out) that is not finite may reach all of them.
  *
  *   workspace  device, 16-byte aligned, at least what ltxattn_masked_workspace(call, 1) says;
  *              calls that may overlap in time need one each.

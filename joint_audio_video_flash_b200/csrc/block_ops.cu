@@ -223,9 +223,10 @@ int grad_plan(int cols, const NormLayout& l, bool affine, long long groups,
   plan->lanes = 0;
   plan->phases = l.edge ? l.phases : 1;
   // a row's fixed costs (sums, barrier, addresses) fall on fewer elements with 2 chunks a
-  // thread, but twice the warps fit: 4 are faster where rows of 2-byte elements come in whole
-  // chunks (30720 x 4096 bf16: 135 us against 158), 2 otherwise (20000 x 1537 bf16: 103 us
-  // against 134; 4-byte elements are bound by memory either way)
+  // thread, but twice the warps fit.  4 against 2, in us: whole chunks of 2-byte elements 30720 x
+  // 4096 143 and 175; ragged rows 20000 x 1537 bf16 142 and 109, fp32 119 and 113, 5001 x 1537
+  // fp32 41 and 38; whole chunks of fp32 30720 x 4096 234 and 234 (6.5 TB/s, memory), 30720 x 2048
+  // 125 and 145, 20000 x 1024 53 and 57: 2 is not the better one for narrow fp32 rows
   const int first = sizeof(T) == 2 && !l.edge ? 4 : 2;
   for (int chunks : {first, 6 - first}) {
     if (!l.vector || !(plan->lanes = norm_lanes(cols, shift, chunks * V))) continue;
