@@ -201,12 +201,12 @@ ltx::MaskedShape shape_of(const ltxattn_masked_call& a, const ltx::DeviceContext
 // most of a row's weight: a running maximum with a cap, and dQ free of out's rounding without one.
 // It is the average that counts, so the early rows of a long causal document, and a short document
 // among long ones, have what the long ones have (their weights and P are rounded to bf16 then, as
-// everybody's).  Measured at head_dim 128, 16 heads, 4096 rows in all; the maximum against none,
-// capped scores of deviation 4 forwards: 1024 keys 76 and 68 us, 2048 keys 127 and 111 us, 8192
-// keys (8192 rows) 780 and 694 us, for 1.7e-3 instead of 2.3e-3 of the result's norm; the sum
-// against none, plain scores backwards: 191 and 178, 299 and 274, 1698 and 1532 us, for 2.36e-3
-// instead of 2.37e-3 (2.40e-3 and 2.43e-3 at 128 keys).  2048 is a choice between the two, not an
-// edge in either.
+// everybody's). Measured at head_dim 128, 16 heads, 4096 rows in all, each call alone with a cold
+// L2 (about 10 us more than among others); the maximum against none, capped scores of deviation 4
+// forwards: 1024 keys 76 and 68 us, 2048 keys 127 and 111 us, 8192 keys (8192 rows) 780 and 694 us,
+// for 1.7e-3 instead of 2.3e-3 of the result's norm; the sum against none, plain scores backwards:
+// 191 and 178, 299 and 274, 1698 and 1532 us, for 2.36e-3 instead of 2.37e-3 (2.40e-3 and 2.43e-3
+// at 128 keys). 2048 is a choice between the two, not an edge in either.
 constexpr int kFewKeys = 2048;
 bool few_keys(const ltx::MaskedShape& s) { return s.kv_len / std::max(s.docs, 1) <= kFewKeys; }
 
